@@ -17,7 +17,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libwush.so")
 
 if not os.path.exists(LIB_PATH):
-    raise ImportError(f"{LIB_PATH} is not built; run `python -m activation_quantization_b200.build`")
+    raise ImportError(f"{LIB_PATH} is not built; run `python activation_quantization_b200/build.py`")
 
 _lib = ctypes.CDLL(LIB_PATH)
 

@@ -1,6 +1,7 @@
 """Build libwush.so in-tree: nvcc for the sm_100a CUDA sources, g++ for the host code.
 
-Usage: python -m activation_quantization_b200.build   (or build() from Python)
+Usage: python activation_quantization_b200/build.py   (as a file: the package cannot be
+imported before the library is there)
 The library lands next to this file; its build directory is ``_build/``.
 """
 from __future__ import annotations
