@@ -24,8 +24,15 @@ _lib = ctypes.CDLL(LIB_PATH)
 FORMATS = {"mxfp4": 0, "nvfp4": 1, "int4": 2}
 TRANSFORMS = {"identity": 0, "hadamard": 1, "wus": 2, "wush": 3, "wush_diag": 4}
 IN_BF16, IN_FP32 = 0, 1
+ROWNORMS = {"none": 0, "rms": 1, "layer": 2}
+GATES = {"linear": 0, "sigmoid": 1, "silu": 2}
 
 _i64, _i32, _f32, _vp, _sz = ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+
+class _NormSpec(ctypes.Structure):
+    _fields_ = [("kind", _i32), ("dtype", _i32), ("weight", _vp), ("bias", _vp), ("weight_offset", _f32),
+                ("eps", _f32)]
+
 
 _SIGNATURES = {
     "wush_status_string": (ctypes.c_char_p, [_i32]),
@@ -54,6 +61,9 @@ _SIGNATURES = {
     "itq3_quantize_weights": (_i32, [_vp, _i64, _i64, _vp, _vp]),
     "itq3_dequant_gemv": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp]),
     "itq3_dequant_gemv_noalloc": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp]),
+    "wush_residual_norm": (_i32, [_vp, _i32, _i64, _vp, _vp, _i32, _i64, _i32, _vp, _i32, _i64, _f32, _f32, _i64,
+                                  _i64, _vp, _vp, _i64, _vp, _i32, _i64, _vp]),
+    "wush_norm": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp]),
     "wush_check_device_status": (_i32, [_vp]),
     "wush_debug_set_wait_limit": (_i32, [_i64]),
     "wush_debug_set_gemm_variant": (_i32, [_i32]),
@@ -430,6 +440,126 @@ def itq3_dequant_gemv_noalloc(codes, scales, x, d_out: int, y, stream=None):
     _check("itq3_dequant_gemv_noalloc",
            _lib.itq3_dequant_gemv_noalloc(_ptr(codes), _ptr(scales), _ptr(x), tokens, d_out, d_in, _ptr(y),
                                           _stream(stream)))
+
+
+_DTYPES = {}
+
+
+def _dtype(fn, name, t):
+    """wush_dtype of a tensor; ValueError for a type the library does not take."""
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: 0, torch.float32: 1, torch.float16: 2})
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{fn}: {name} must be bf16, fp32 or fp16, got {t.dtype}")
+    return dt
+
+
+def _rows(fn, name, t, shape):
+    """(pointer, wush_dtype, row stride) of a [rows, d] tensor whose rows are contiguous."""
+    if t is None:
+        return None, 0, 0
+    dt = _dtype(fn, name, t)
+    if t.shape != shape:
+        raise ValueError(f"{fn}: {name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    rows, d = shape
+    row_stride, col_stride = t.stride()
+    if d > 1 and col_stride != 1:
+        raise ValueError(f"{fn}: the rows of {name} must be contiguous")
+    if rows > 1 and row_stride < d:
+        raise ValueError(f"{fn}: the rows of {name} overlap")
+    return t.data_ptr(), dt, row_stride if rows > 1 else max(row_stride, d)
+
+
+def _norm_spec(fn, which, kind, weight, bias, d, eps, weight_offset):
+    dt = 0
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is None:
+            continue
+        dt = _dtype(fn, f"{which} {name}", t)
+        if t.shape != (d,) or (d > 1 and t.stride(0) != 1):
+            raise ValueError(f"{fn}: {which} {name} must be a contiguous vector of {d}, got {tuple(t.shape)}")
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError(f"{fn}: {which} weight and bias must have one type")
+    return _NormSpec(_enum(ROWNORMS, kind), dt, None if weight is None else weight.data_ptr(),
+                     None if bias is None else bias.data_ptr(), weight_offset, eps)
+
+
+def _on_device(*tensors):
+    """The device that all the given tensors (None left out) share, as an index."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        i = t.get_device()
+        if dev is None:
+            dev = i
+        elif dev != i:
+            raise ValueError(f"tensors on cuda:{dev} and cuda:{i}")
+    return dev
+
+
+def _launch(fn, dev, stream, call):
+    """Runs ``call(stream pointer)`` with ``dev`` current, on its current stream unless one is given."""
+    import torch
+    if dev == torch.cuda.current_device():
+        _check(fn, call(_stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, call(_stream(stream)))
+
+
+def wush_norm(x, h, kind, weight=None, bias=None, eps: float = 1e-6, weight_offset: float = 0.0, stream=None):
+    """h = N(x) row by row: x, h CUDA [rows, d] (bf16, fp32 or fp16; rows contiguous, any row
+    stride; h may be x), kind "rms" or "layer", weight and bias CUDA [d] or None."""
+    fn = "wush_norm"
+    shape = x.shape
+    xp, xd, xs = _rows(fn, "x", x, shape)
+    hp, hd, hs = _rows(fn, "h", h, shape)
+    spec = _norm_spec(fn, "the", kind, weight, bias, shape[1], eps, weight_offset)
+    dev = _on_device(x, h, weight, bias)
+    if shape[0] == 0:                               # an empty tensor has no pointer
+        return
+    _launch(fn, dev, stream, lambda st: _lib.wush_norm(xp, xd, xs, shape[0], shape[1], ctypes.byref(spec), hp, hd, hs,
+                                                       st))
+
+
+def wush_residual_norm(y, r=None, r_out=None, h=None, *, post="none", post_weight=None, post_bias=None, gate=None,
+                       gate_act="linear", residual_scale: float = 1.0, branch_scale: float = 1.0, pre="none",
+                       pre_weight=None, pre_bias=None, eps: float = 1e-6, weight_offset: float = 0.0, stream=None):
+    """r_out = residual_scale * r + branch_scale * N_post(y) * act(gate); h = N_pre(r_out).
+
+    y, r, r_out, h: CUDA [rows, d] (bf16, fp32 or fp16 each, r_out of r's type; rows contiguous,
+    any row stride); r_out may be r; r, r_out or h may be None.  gate: CUDA [d] (one for all
+    rows), [rows, d] or None.  eps and weight_offset hold for both norms."""
+    fn = "wush_residual_norm"
+    shape = y.shape
+    rows, d = shape
+    yp, yd, ys = _rows(fn, "y", y, shape)
+    rp, rd, rs = _rows(fn, "r", r, shape)
+    op, od, os_ = _rows(fn, "r_out", r_out, shape)
+    hp, hd, hs = _rows(fn, "h", h, shape)
+    if r is not None and r_out is not None and rd != od:
+        raise ValueError(f"{fn}: r_out must have r's type, got {r_out.dtype}")
+    if gate is not None and gate.dim() == 1:
+        gp, gd, gs = gate.data_ptr(), _dtype(fn, "gate", gate), 0
+        if gate.shape != (d,) or (d > 1 and gate.stride(0) != 1):
+            raise ValueError(f"{fn}: a gate per channel must be a contiguous vector of {d}, got {tuple(gate.shape)}")
+    else:
+        gp, gd, gs = _rows(fn, "gate", gate, shape)
+    post_spec = _norm_spec(fn, "the post", post, post_weight, post_bias, d, eps, weight_offset)
+    pre_spec = _norm_spec(fn, "the pre", pre, pre_weight, pre_bias, d, eps, weight_offset)
+    dev = _on_device(y, r, r_out, h, gate, post_weight, post_bias, pre_weight, pre_bias)
+    act = _enum(GATES, gate_act)
+    if rows == 0:                                   # an empty tensor has no pointer
+        return
+    _launch(fn, dev, stream,
+            lambda st: _lib.wush_residual_norm(yp, yd, ys, ctypes.byref(post_spec), gp, gd, gs, act, rp,
+                                               rd if r is not None else od, rs, residual_scale, branch_scale, rows, d,
+                                               ctypes.byref(pre_spec), op, os_, hp, hd, hs, st))
 
 
 def wush_check_device_status(stream=None) -> int:

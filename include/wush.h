@@ -29,7 +29,7 @@
  *   - Every argument is checked before any launch. A failed check returns
  *     WUSH_ERR_INVALID_ARG / WUSH_ERR_UNSUPPORTED and launches nothing.
  *   - A CUDA launch error returns WUSH_ERR_CUDA (cudaGetLastError after launch).
- *   - Device pointers must be 16-byte aligned.
+ *   - Device pointers must be 16-byte aligned, unless a call says otherwise.
  *   - ``stream`` is a cudaStream_t passed as void*; NULL is the legacy default
  *     stream.  Work is enqueued in stream order.
  *   - Inputs must be finite.  The host calls (calibration, ITQ3 weight
@@ -420,6 +420,73 @@ int itq3_dequant_gemv(const uint8_t* codes, const void* scales_fp16, const void*
  * above). */
 int itq3_dequant_gemv_noalloc(const uint8_t* codes, const void* scales_fp16, const void* x_fp16,
                               int64_t tokens, int64_t d_out, int64_t d_in, float* y, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Norms before and after a block, fused with its gate and residual (device, one
+ * launch)
+ *
+ * The pages turn on the quantised projection; these calls make the activations it
+ * reads (bf16 or fp32 for wush_transform_quant, fp16 for the ITQ3 GEMV) and consume
+ * the fp32 y it writes.  For each of ``rows`` rows of d elements:
+ *   u     = N_post(y) * act(gate)
+ *   r_out = residual_scale * r + branch_scale * u
+ *   h     = N_pre(r_out)
+ * with N by kind
+ *   RMS:   v / sqrt(mean(v^2) + eps) * (w + weight_offset) + b
+ *   LAYER: (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * (w + weight_offset) + b
+ *   NONE:  v
+ * (no weight: a factor of 1, weight_offset unused; no bias: 0).  Everything is fp32
+ * inside: h is taken from the fp32 sum, not from the rounded r_out, and each output
+ * is rounded once.  Squares are summed in fp32, so values beyond 1e19 in magnitude
+ * overflow them; a NaN or an infinity reaches its own row only.  A row of zeros
+ * with eps = 0 gives NaN, as the formula does.
+ * ------------------------------------------------------------------------- */
+
+/* Element types of the calls from here on (the first two are WUSH_IN_BF16 and
+ * WUSH_IN_FP32). */
+typedef enum { WUSH_BF16 = 0, WUSH_FP32 = 1, WUSH_FP16 = 2 } wush_dtype;
+
+typedef enum { WUSH_ROWNORM_NONE = 0, WUSH_ROWNORM_RMS = 1, WUSH_ROWNORM_LAYER = 2 } wush_rownorm_kind;
+
+typedef enum { WUSH_GATE_LINEAR = 0, WUSH_GATE_SIGMOID = 1, WUSH_GATE_SILU = 2 } wush_gate_act;
+
+/* A norm: weight and bias are device vectors of d elements of one type, or NULL. */
+typedef struct {
+  int kind;            /* wush_rownorm_kind */
+  int dtype;           /* wush_dtype of weight and bias */
+  const void* weight;
+  const void* bias;
+  float weight_offset; /* finite */
+  float eps;           /* >= 0, finite */
+} wush_norm_spec;
+
+/* y:       device [rows, d] of y_dtype, row stride y_stride (in elements, as all
+ *          strides here; >= d).
+ * post:    N_post, or NULL for none.
+ * gate:    device [rows, d] of gate_dtype with row stride gate_stride, or one row of
+ *          d elements for all rows with gate_stride 0; act(g) is g, sigmoid(g) or
+ *          g sigmoid(g) by gate_act.  NULL: no gate.
+ * r:       device [rows, d] of r_dtype; NULL: no residual (r_out = branch_scale u).
+ * r_out:   device [rows, d] of r_dtype; may be r itself (with r's stride).  NULL:
+ *          not written.
+ * pre, h:  N_pre (NULL for none) and its output, device [rows, d] of h_dtype.  h
+ *          NULL: not computed.
+ * Requirements: 1 <= d <= 32768, 0 <= rows < 2^31 (0: nothing is launched), at least
+ * one of r_out and h, finite scales, pointers aligned to their element; 16-byte
+ * aligned rows and d % 8 == 0 run with 16-byte accesses.  Outputs may not overlap
+ * each other or an input other than r_out = r (rows that interleave with equal
+ * strides, i.e. columns of one wide buffer, do not overlap): WUSH_ERR_INVALID_ARG. */
+int wush_residual_norm(const void* y, int y_dtype, int64_t y_stride, const wush_norm_spec* post,
+                       const void* gate, int gate_dtype, int64_t gate_stride, int gate_act,
+                       const void* r, int r_dtype, int64_t r_stride, float residual_scale,
+                       float branch_scale, int64_t rows, int64_t d, const wush_norm_spec* pre,
+                       void* r_out, int64_t r_out_stride, void* h, int h_dtype, int64_t h_stride,
+                       void* stream);
+
+/* h = N(x): the norm before a block alone.  h may be x itself (same type and
+ * stride).  Arguments and requirements as above. */
+int wush_norm(const void* x, int x_dtype, int64_t x_stride, int64_t rows, int64_t d,
+              const wush_norm_spec* norm, void* h, int h_dtype, int64_t h_stride, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Diagnostics

@@ -24,4 +24,4 @@ Parity status per function: every public function is pinned by a
 ``-m "not gpu"`` test against closed forms, library routines or brute force
 (tests/test_oracle_*.py). None is "parity unpinned".
 """
-from . import formats, transforms, calibrate, quant, gemm, itq3, loss  # noqa: F401
+from . import formats, transforms, calibrate, quant, gemm, itq3, loss, block  # noqa: F401
