@@ -64,6 +64,9 @@ _SIGNATURES = {
     "wush_residual_norm": (_i32, [_vp, _i32, _i64, _vp, _vp, _i32, _i64, _i32, _vp, _i32, _i64, _f32, _f32, _i64,
                                   _i64, _vp, _vp, _i64, _vp, _i32, _i64, _vp]),
     "wush_norm": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp]),
+    "wush_lora_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64]),
+    "wush_lora_add": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp,
+                             _i64, _vp, _sz, _vp]),
     "wush_check_device_status": (_i32, [_vp]),
     "wush_debug_set_wait_limit": (_i32, [_i64]),
     "wush_debug_set_gemm_variant": (_i32, [_i32]),
@@ -469,7 +472,7 @@ def _rows(fn, name, t, shape):
         raise ValueError(f"{fn}: the rows of {name} must be contiguous")
     if rows > 1 and row_stride < d:
         raise ValueError(f"{fn}: the rows of {name} overlap")
-    return t.data_ptr(), dt, row_stride if rows > 1 else max(row_stride, d)
+    return t.data_ptr(), dt, row_stride if rows > 1 else d
 
 
 def _norm_spec(fn, which, kind, weight, bias, d, eps, weight_offset):
@@ -560,6 +563,49 @@ def wush_residual_norm(y, r=None, r_out=None, h=None, *, post="none", post_weigh
             lambda st: _lib.wush_residual_norm(yp, yd, ys, ctypes.byref(post_spec), gp, gd, gs, act, rp,
                                                rd if r is not None else od, rs, residual_scale, branch_scale, rows, d,
                                                ctypes.byref(pre_spec), op, os_, hp, hd, hs, st))
+
+
+def wush_lora_workspace_bytes(tokens: int, d_in: int, d_out: int, n_adapters: int, rank: int) -> int:
+    return int(_lib.wush_lora_workspace_bytes(tokens, d_in, d_out, n_adapters, rank))
+
+
+def _exactly(fn, name, t, shape, dtype):
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def wush_lora_add(x, adapter, a, b, y_in, y, workspace=None, ranks=None, scale=None, stream=None):
+    """y = y_in + scale[g] * (x @ a[g].T) @ b[g].T row by row, g = adapter[row] (none where outside the pool).
+
+    x CUDA [tokens, d_in] bf16 or fp16; adapter int32 [tokens]; a [n, rank, d_in] and b [n, d_out, rank] of x's
+    type; y_in (None: zeros; may be y) and y fp32 [tokens, d_out]; rows of x, y_in and y contiguous, any row
+    stride that keeps them 16-byte aligned; ranks int32 [n] or None; scale fp32 [n] or None; workspace at least
+    wush_lora_workspace_bytes(tokens, d_in, d_out, n, rank) bytes (None where that is 0)."""
+    import torch
+    fn = "wush_lora_add"
+    tokens, d_in = x.shape
+    n, d_out, rank = b.shape
+    xp, xd, xs = _rows(fn, "x", x, x.shape)
+    out = torch.Size((tokens, d_out))
+    for name, t in (("y_in", y_in), ("y", y)):
+        if t is not None and t.dtype != torch.float32:
+            raise ValueError(f"{fn}: {name} must be torch.float32, got {t.dtype}")
+    ip, _, is_ = _rows(fn, "y_in", y_in, out)
+    yp, _, ys = _rows(fn, "y", y, out)
+    gp = _exactly(fn, "adapter", adapter, (tokens,), torch.int32)
+    ap = _exactly(fn, "a", a, (n, rank, d_in), x.dtype)
+    bp = _exactly(fn, "b", b, (n, d_out, rank), x.dtype)
+    kp = _exactly(fn, "ranks", ranks, (n,), torch.int32)
+    sp = _exactly(fn, "scale", scale, (n,), torch.float32)
+    wp, wn = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
+    dev = _on_device(x, adapter, a, b, y_in, y, ranks, scale)
+    if tokens == 0:                                 # an empty tensor has no pointer
+        return
+    _launch(fn, dev, stream, lambda st: _lib.wush_lora_add(xp, xd, xs, tokens, d_in, d_out, gp, ap, bp, n, rank, kp, sp,
+                                                           ip, is_, yp, ys, wp, wn, st))
 
 
 def wush_check_device_status(stream=None) -> int:

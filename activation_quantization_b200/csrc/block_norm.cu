@@ -174,27 +174,6 @@ __global__ void __launch_bounds__(kMaxThreads) residual_norm_kernel(const __grid
 
 // ------------------------------------------------------------------ host checks
 
-struct Span {                                              // rows of a tensor, as bytes
-  const char* p;
-  int64_t stride, width;                                   // bytes
-};
-
-Span span(const void* p, int dt, int64_t stride, int64_t d) {
-  return {static_cast<const char*>(p), stride * dtype_bytes(dt), d * dtype_bytes(dt)};
-}
-
-// Whether two sets of rows share a byte.  Rows of one stride can interleave (columns
-// of one wide buffer); sets of unequal strides are kept apart as whole ranges.
-bool overlap(const Span& a, const Span& b, int64_t rows) {
-  if (!a.p || !b.p) return false;
-  const char* a_end = a.p + (rows - 1) * a.stride + a.width;
-  const char* b_end = b.p + (rows - 1) * b.stride + b.width;
-  if (a_end <= b.p || b_end <= a.p) return false;
-  if (a.stride != b.stride) return true;
-  const int64_t delta = ((b.p - a.p) % a.stride + a.stride) % a.stride;
-  return delta < a.width || a.stride - delta < b.width;
-}
-
 bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 int check_norm(const wush_norm_spec* s, NormArgs* out, bool* vec) {

@@ -1,5 +1,5 @@
 // What the operators around a quantised projection share: element types, their
-// conversions, and the programmatic-launch configuration.
+// conversions, and the host checks on overlapping rows.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -11,6 +11,27 @@ namespace wush {
 
 inline int dtype_bytes(int dt) { return dt == WUSH_FP32 ? 4 : 2; }
 inline bool known_dtype(int dt) { return dt == WUSH_BF16 || dt == WUSH_FP32 || dt == WUSH_FP16; }
+
+struct Span {                                              // rows of a tensor, as bytes
+  const char* p;
+  int64_t stride, width;                                   // bytes
+};
+
+inline Span span(const void* p, int dt, int64_t stride, int64_t d) {
+  return {static_cast<const char*>(p), stride * dtype_bytes(dt), d * dtype_bytes(dt)};
+}
+
+// Whether two sets of rows share a byte.  Rows of one stride can interleave (columns
+// of one wide buffer); sets of unequal strides are kept apart as whole ranges.
+inline bool overlap(const Span& a, const Span& b, int64_t rows) {
+  if (!a.p || !b.p) return false;
+  const char* a_end = a.p + (rows - 1) * a.stride + a.width;
+  const char* b_end = b.p + (rows - 1) * b.stride + b.width;
+  if (a_end <= b.p || b_end <= a.p) return false;
+  if (a.stride != b.stride) return true;
+  const int64_t delta = ((b.p - a.p) % a.stride + a.stride) % a.stride;
+  return delta < a.width || a.stride - delta < b.width;
+}
 
 // One element.
 __device__ __forceinline__ float load1(const void* p, int dt, int64_t i) {

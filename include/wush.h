@@ -489,6 +489,45 @@ int wush_norm(const void* x, int x_dtype, int64_t x_stride, int64_t rows, int64_
               const wush_norm_spec* norm, void* h, int h_dtype, int64_t h_stride, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection (device)
+ *
+ * The projection's weights are quantised once and shared by every request
+ * (wush_qgemm, wush_qgemm_int4, itq3_dequant_gemv); a request's own adapter stays in
+ * 16 bits and is added to the projection's fp32 y.  With g = adapter[t]:
+ *   s[t, j] = sum_i x[t, i] a[g, j, i]                                  j < k_g
+ *   y[t, o] = y_in[t, o] + scale[g] * sum_{j < k_g} s[t, j] b[g, o, j]
+ * and y[t] = y_in[t] where g is outside [0, n_adapters) (no adapter; -1 by
+ * convention) or k_g is 0.  Products are exact, sums are fp32, and s enters the
+ * second product with at least 22 bits.  A token's result does not depend on which
+ * other tokens share the call beyond fp32 rounding, and equal calls give equal bits.
+ * A NaN or an infinity in a token's x or y_in reaches that token only, one in an
+ * adapter that adapter's tokens only.
+ *
+ * x:        device [tokens, d_in], bf16 or fp16 (x_dtype), row stride x_stride (in
+ *           elements, a multiple of 8).
+ * adapter:  device int32 [tokens], in any order.
+ * a, b:     device [n_adapters, rank, d_in] and [n_adapters, d_out, rank] of
+ *           x_dtype: the two factors, each row contiguous.
+ * ranks:    device int32 [n_adapters]: k_g, clamped to [0, rank]; NULL: all rank.
+ *           Rows of a and columns of b from k_g on are never used, whatever they hold.
+ * scale:    device fp32 [n_adapters] or NULL (1).
+ * y_in:     device fp32 [tokens, d_out], row stride a multiple of 4; NULL: zeros.
+ * y:        device fp32 [tokens, d_out], row stride a multiple of 4; may be y_in (with
+ *           its stride), otherwise it may overlap neither y_in nor x.
+ * workspace: device, at least wush_lora_workspace_bytes(...) bytes, 16-byte aligned;
+ *           may be NULL where that is 0.  Calls that can overlap in time (two streams,
+ *           two graphs) need one each.
+ * Requirements: tokens >= 0 (0: nothing is launched), d_in % 32 == 0, d_out % 8 == 0,
+ * rank % 8 == 0, 8 <= rank <= 256; WUSH_ERR_BUFFER_TOO_SMALL for a small workspace. */
+size_t wush_lora_workspace_bytes(int64_t tokens, int64_t d_in, int64_t d_out, int64_t n_adapters,
+                                 int64_t rank);
+int wush_lora_add(const void* x, int x_dtype, int64_t x_stride, int64_t tokens, int64_t d_in,
+                  int64_t d_out, const int32_t* adapter, const void* a, const void* b,
+                  int64_t n_adapters, int64_t rank, const int32_t* ranks, const float* scale,
+                  const float* y_in, int64_t y_in_stride, float* y, int64_t y_stride, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Diagnostics
  * ------------------------------------------------------------------------- */
 

@@ -46,3 +46,21 @@ def test_non_finite_inputs_are_refused(bad):
                  lambda: B.norm(ok, "rms", x[1])):
         with pytest.raises(NonFiniteInput):
             call()
+
+
+def test_lora_add_is_the_per_token_formula():
+    rng = np.random.default_rng(3)
+    x, a, b = rng.standard_normal((6, 8)), rng.standard_normal((3, 4, 8)), rng.standard_normal((3, 5, 4))
+    a[1, 2:] = np.nan                                    # padding is never read
+    b[1, :, 2:] = np.inf
+    y_in, adapter, ranks = rng.standard_normal((6, 5)), np.array([2, -1, 0, 1, 3, 1]), np.array([4, 2, 0])
+    scale = np.array([0.5, -2.0, 3.0])
+    y, size = B.lora_add(x, adapter, a, b, y_in, ranks, scale)
+    want = y_in.copy()
+    want[2] += 0.5 * b[0] @ (a[0] @ x[2])
+    for t in (3, 5):
+        want[t] += -2.0 * b[1][:, :2] @ (a[1][:2] @ x[t])
+    assert np.allclose(y, want, rtol=1e-13) and np.array_equal(y[[0, 1, 4]], y_in[[0, 1, 4]])
+    assert np.all(size >= np.abs(y - y_in) * (1 - 1e-12))
+    with pytest.raises(NonFiniteInput):
+        B.lora_add(np.full((6, 8), np.nan), adapter, a, b)
