@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -29,10 +30,11 @@ GATES = {"linear": 0, "sigmoid": 1, "silu": 2}
 
 _i64, _i32, _f32, _vp, _sz = ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 
-class _NormSpec(ctypes.Structure):
-    _fields_ = [("kind", _i32), ("dtype", _i32), ("weight", _vp), ("bias", _vp), ("weight_offset", _f32),
-                ("eps", _f32)]
-
+# The calls with many arguments take them in one C struct (wush_norm_spec, wush_residual_norm_args and
+# wush_lora_args in include/wush.h), packed here in its order.
+_NORM_SPEC = struct.Struct("@iiPPff")
+_RESIDUAL_NORM_ARGS = struct.Struct("@5P7qiiPPffiiPPff5i2f")
+_LORA_ARGS = struct.Struct("@9P8qNi")
 
 _SIGNATURES = {
     "wush_status_string": (ctypes.c_char_p, [_i32]),
@@ -61,12 +63,10 @@ _SIGNATURES = {
     "itq3_quantize_weights": (_i32, [_vp, _i64, _i64, _vp, _vp]),
     "itq3_dequant_gemv": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp]),
     "itq3_dequant_gemv_noalloc": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp]),
-    "wush_residual_norm": (_i32, [_vp, _i32, _i64, _vp, _vp, _i32, _i64, _i32, _vp, _i32, _i64, _f32, _f32, _i64,
-                                  _i64, _vp, _vp, _i64, _vp, _i32, _i64, _vp]),
+    "wush_residual_norm": (_i32, [_vp, _vp]),
     "wush_norm": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp]),
     "wush_lora_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64]),
-    "wush_lora_add": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp,
-                             _i64, _vp, _sz, _vp]),
+    "wush_lora_add": (_i32, [_vp, _vp]),
     "wush_check_device_status": (_i32, [_vp]),
     "wush_debug_set_wait_limit": (_i32, [_i64]),
     "wush_debug_set_gemm_variant": (_i32, [_i32]),
@@ -446,88 +446,91 @@ def itq3_dequant_gemv_noalloc(codes, scales, x, d_out: int, y, stream=None):
 
 
 _DTYPES = {}
+_raw_stream = None
 
 
-def _dtype(fn, name, t):
-    """wush_dtype of a tensor; ValueError for a type the library does not take."""
-    if not _DTYPES:
+def _device_call(t):
+    """The device of a CUDA tensor (an index): what the other tensors of a call are compared with."""
+    global _raw_stream
+    if _raw_stream is None:
         import torch
         _DTYPES.update({torch.bfloat16: 0, torch.float32: 1, torch.float16: 2})
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    return t.get_device()
+
+
+def _rows(fn, name, t, shape, dev):
+    """(pointer, wush_dtype, row stride) of a [rows, d] tensor whose rows are contiguous; (0, 0, 0) for None."""
+    if t is None:
+        return 0, 0, 0
     dt = _DTYPES.get(t.dtype)
     if dt is None:
         raise ValueError(f"{fn}: {name} must be bf16, fp32 or fp16, got {t.dtype}")
-    return dt
-
-
-def _rows(fn, name, t, shape):
-    """(pointer, wush_dtype, row stride) of a [rows, d] tensor whose rows are contiguous."""
-    if t is None:
-        return None, 0, 0
-    dt = _dtype(fn, name, t)
     if t.shape != shape:
         raise ValueError(f"{fn}: {name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    rows, d = shape
+    if t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} is on {t.device}, another tensor on {'cpu' if dev < 0 else f'cuda:{dev}'}")
     row_stride, col_stride = t.stride()
+    rows, d = shape
     if d > 1 and col_stride != 1:
         raise ValueError(f"{fn}: the rows of {name} must be contiguous")
-    if rows > 1 and row_stride < d:
+    if rows <= 1:
+        return t.data_ptr(), dt, d
+    if row_stride < d:
         raise ValueError(f"{fn}: the rows of {name} overlap")
-    return t.data_ptr(), dt, row_stride if rows > 1 else d
+    return t.data_ptr(), dt, row_stride
 
 
-def _norm_spec(fn, which, kind, weight, bias, d, eps, weight_offset):
-    dt = 0
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is None:
-            continue
-        dt = _dtype(fn, f"{which} {name}", t)
-        if t.shape != (d,) or (d > 1 and t.stride(0) != 1):
-            raise ValueError(f"{fn}: {which} {name} must be a contiguous vector of {d}, got {tuple(t.shape)}")
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+def _vector(fn, name, t, d, dev):
+    """(pointer, wush_dtype) of a contiguous vector of d elements; (0, 0) for None."""
+    if t is None:
+        return 0, 0
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{fn}: {name} must be bf16, fp32 or fp16, got {t.dtype}")
+    if t.shape != (d,) or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous vector of {d}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} is on {t.device}, another tensor on {'cpu' if dev < 0 else f'cuda:{dev}'}")
+    return t.data_ptr(), dt
+
+
+def _norm_spec(fn, which, kind, weight, bias, d, dev, eps, weight_offset):
+    wp, wd = _vector(fn, which + " weight", weight, d, dev)
+    if bias is None:
+        return ROWNORMS[kind], wd, wp, 0, weight_offset, eps
+    bp, bd = _vector(fn, which + " bias", bias, d, dev)
+    if weight is not None and wd != bd:
         raise ValueError(f"{fn}: {which} weight and bias must have one type")
-    return _NormSpec(_enum(ROWNORMS, kind), dt, None if weight is None else weight.data_ptr(),
-                     None if bias is None else bias.data_ptr(), weight_offset, eps)
+    return ROWNORMS[kind], bd, wp, bp, weight_offset, eps
 
 
-def _on_device(*tensors):
-    """The device that all the given tensors (None left out) share, as an index."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("expected a CUDA tensor")
-        i = t.get_device()
-        if dev is None:
-            dev = i
-        elif dev != i:
-            raise ValueError(f"tensors on cuda:{dev} and cuda:{i}")
-    return dev
-
-
-def _launch(fn, dev, stream, call):
-    """Runs ``call(stream pointer)`` with ``dev`` current, on its current stream unless one is given."""
+def _launch(fn, name, args, dev, stream):
+    """Calls ``fn(*args, stream)`` with device ``dev`` current, on its current stream unless one is given."""
     import torch
-    if dev == torch.cuda.current_device():
-        _check(fn, call(_stream(stream)))
-    else:
+    if dev < 0:
+        raise ValueError("expected a CUDA tensor")
+    if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            _check(fn, call(_stream(stream)))
+            status = fn(*args, _stream(stream))
+    else:
+        status = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
+    if status != 0:
+        raise WushError(name, status)
 
 
 def wush_norm(x, h, kind, weight=None, bias=None, eps: float = 1e-6, weight_offset: float = 0.0, stream=None):
     """h = N(x) row by row: x, h CUDA [rows, d] (bf16, fp32 or fp16; rows contiguous, any row
     stride; h may be x), kind "rms" or "layer", weight and bias CUDA [d] or None."""
     fn = "wush_norm"
-    shape = x.shape
-    xp, xd, xs = _rows(fn, "x", x, shape)
-    hp, hd, hs = _rows(fn, "h", h, shape)
-    spec = _norm_spec(fn, "the", kind, weight, bias, shape[1], eps, weight_offset)
-    dev = _on_device(x, h, weight, bias)
-    if shape[0] == 0:                               # an empty tensor has no pointer
-        return
-    _launch(fn, dev, stream, lambda st: _lib.wush_norm(xp, xd, xs, shape[0], shape[1], ctypes.byref(spec), hp, hd, hs,
-                                                       st))
+    dev, shape = _device_call(x), x.shape
+    xp, xd, xs = _rows(fn, "x", x, shape, dev)
+    hp, hd, hs = _rows(fn, "h", h, shape, dev)
+    rows, d = shape
+    spec = _NORM_SPEC.pack(*_norm_spec(fn, "the", kind, weight, bias, d, dev, eps, weight_offset))
+    if rows:                                        # (an empty tensor has no pointer)
+        _launch(_lib.wush_norm, fn, (xp, xd, xs, rows, d, spec, hp, hd, hs), dev, stream)
 
 
 def wush_residual_norm(y, r=None, r_out=None, h=None, *, post="none", post_weight=None, post_bias=None, gate=None,
@@ -539,41 +542,43 @@ def wush_residual_norm(y, r=None, r_out=None, h=None, *, post="none", post_weigh
     any row stride); r_out may be r; r, r_out or h may be None.  gate: CUDA [d] (one for all
     rows), [rows, d] or None.  eps and weight_offset hold for both norms."""
     fn = "wush_residual_norm"
-    shape = y.shape
+    dev, shape = _device_call(y), y.shape
+    yp, yd, ys = _rows(fn, "y", y, shape, dev)
     rows, d = shape
-    yp, yd, ys = _rows(fn, "y", y, shape)
-    rp, rd, rs = _rows(fn, "r", r, shape)
-    op, od, os_ = _rows(fn, "r_out", r_out, shape)
-    hp, hd, hs = _rows(fn, "h", h, shape)
-    if r is not None and r_out is not None and rd != od:
+    rp, rd, rs = _rows(fn, "r", r, shape, dev)
+    op, od, os_ = _rows(fn, "r_out", r_out, shape, dev)
+    hp, hd, hs = _rows(fn, "h", h, shape, dev)
+    if r is None:
+        rd = od
+    elif r_out is not None and rd != od:
         raise ValueError(f"{fn}: r_out must have r's type, got {r_out.dtype}")
-    if gate is not None and gate.dim() == 1:
-        gp, gd, gs = gate.data_ptr(), _dtype(fn, "gate", gate), 0
-        if gate.shape != (d,) or (d > 1 and gate.stride(0) != 1):
-            raise ValueError(f"{fn}: a gate per channel must be a contiguous vector of {d}, got {tuple(gate.shape)}")
+    gs = 0
+    if gate is None:
+        gp = gd = 0
+    elif gate.dim() == 1:
+        gp, gd = _vector(fn, "a gate per channel", gate, d, dev)
     else:
-        gp, gd, gs = _rows(fn, "gate", gate, shape)
-    post_spec = _norm_spec(fn, "the post", post, post_weight, post_bias, d, eps, weight_offset)
-    pre_spec = _norm_spec(fn, "the pre", pre, pre_weight, pre_bias, d, eps, weight_offset)
-    dev = _on_device(y, r, r_out, h, gate, post_weight, post_bias, pre_weight, pre_bias)
-    act = _enum(GATES, gate_act)
-    if rows == 0:                                   # an empty tensor has no pointer
-        return
-    _launch(fn, dev, stream,
-            lambda st: _lib.wush_residual_norm(yp, yd, ys, ctypes.byref(post_spec), gp, gd, gs, act, rp,
-                                               rd if r is not None else od, rs, residual_scale, branch_scale, rows, d,
-                                               ctypes.byref(pre_spec), op, os_, hp, hd, hs, st))
+        gp, gd, gs = _rows(fn, "gate", gate, shape, dev)
+    args = _RESIDUAL_NORM_ARGS.pack(
+        yp, gp, rp, op, hp, ys, gs, rs, os_, hs, rows, d,
+        *_norm_spec(fn, "the post", post, post_weight, post_bias, d, dev, eps, weight_offset),
+        *_norm_spec(fn, "the pre", pre, pre_weight, pre_bias, d, dev, eps, weight_offset),
+        yd, gd, rd, hd, GATES[gate_act], residual_scale, branch_scale)
+    if rows:                                        # (an empty tensor has no pointer)
+        _launch(_lib.wush_residual_norm, fn, (args,), dev, stream)
 
 
 def wush_lora_workspace_bytes(tokens: int, d_in: int, d_out: int, n_adapters: int, rank: int) -> int:
     return int(_lib.wush_lora_workspace_bytes(tokens, d_in, d_out, n_adapters, rank))
 
 
-def _exactly(fn, name, t, shape, dtype):
+def _exactly(fn, name, t, shape, dtype, dev):
     if t is None:
-        return None
+        return 0
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{fn}: {name} must be a contiguous {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} is on {t.device}, another tensor on {'cpu' if dev < 0 else f'cuda:{dev}'}")
     return t.data_ptr()
 
 
@@ -586,26 +591,26 @@ def wush_lora_add(x, adapter, a, b, y_in, y, workspace=None, ranks=None, scale=N
     wush_lora_workspace_bytes(tokens, d_in, d_out, n, rank) bytes (None where that is 0)."""
     import torch
     fn = "wush_lora_add"
-    tokens, d_in = x.shape
+    dev, shape = _device_call(x), x.shape
+    xp, xd, xs = _rows(fn, "x", x, shape, dev)
+    tokens, d_in = shape
     n, d_out, rank = b.shape
-    xp, xd, xs = _rows(fn, "x", x, x.shape)
-    out = torch.Size((tokens, d_out))
-    for name, t in (("y_in", y_in), ("y", y)):
-        if t is not None and t.dtype != torch.float32:
-            raise ValueError(f"{fn}: {name} must be torch.float32, got {t.dtype}")
-    ip, _, is_ = _rows(fn, "y_in", y_in, out)
-    yp, _, ys = _rows(fn, "y", y, out)
-    gp = _exactly(fn, "adapter", adapter, (tokens,), torch.int32)
-    ap = _exactly(fn, "a", a, (n, rank, d_in), x.dtype)
-    bp = _exactly(fn, "b", b, (n, d_out, rank), x.dtype)
-    kp = _exactly(fn, "ranks", ranks, (n,), torch.int32)
-    sp = _exactly(fn, "scale", scale, (n,), torch.float32)
-    wp, wn = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
-    dev = _on_device(x, adapter, a, b, y_in, y, ranks, scale)
-    if tokens == 0:                                 # an empty tensor has no pointer
-        return
-    _launch(fn, dev, stream, lambda st: _lib.wush_lora_add(xp, xd, xs, tokens, d_in, d_out, gp, ap, bp, n, rank, kp, sp,
-                                                           ip, is_, yp, ys, wp, wn, st))
+    ip, id_, is_ = _rows(fn, "y_in", y_in, (tokens, d_out), dev)
+    yp, yd, ys = _rows(fn, "y", y, (tokens, d_out), dev)
+    if yd != 1 or (ip and id_ != 1):
+        raise ValueError(f"{fn}: y_in and y must be torch.float32")
+    wp, wn = 0, 0
+    if workspace is not None:
+        if not workspace.is_contiguous() or workspace.get_device() != dev:
+            raise ValueError(f"{fn}: workspace must be contiguous and on x's device")
+        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    args = _LORA_ARGS.pack(
+        xp, _exactly(fn, "adapter", adapter, (tokens,), torch.int32, dev),
+        _exactly(fn, "a", a, (n, rank, d_in), x.dtype, dev), _exactly(fn, "b", b, (n, d_out, rank), x.dtype, dev),
+        _exactly(fn, "ranks", ranks, (n,), torch.int32, dev), _exactly(fn, "scale", scale, (n,), torch.float32, dev),
+        ip, yp, wp, xs, is_, ys, tokens, d_in, d_out, n, rank, wn, xd)
+    if tokens:                                      # (an empty tensor has no pointer)
+        _launch(_lib.wush_lora_add, fn, (args,), dev, stream)
 
 
 def wush_check_device_status(stream=None) -> int:

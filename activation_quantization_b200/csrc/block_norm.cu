@@ -178,7 +178,7 @@ bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) &
 
 int check_norm(const wush_norm_spec* s, NormArgs* out, bool* vec) {
   *out = NormArgs{WUSH_ROWNORM_NONE, WUSH_FP32, nullptr, nullptr, 0.0f, 0.0f};
-  if (!s || s->kind == WUSH_ROWNORM_NONE) return WUSH_OK;
+  if (s->kind == WUSH_ROWNORM_NONE) return WUSH_OK;
   if (s->kind != WUSH_ROWNORM_RMS && s->kind != WUSH_ROWNORM_LAYER) return WUSH_ERR_UNSUPPORTED;
   if (!(s->eps >= 0.0f) || !(s->eps < 3.0e38f)) return WUSH_ERR_INVALID_ARG;
   if (!(s->weight_offset > -3.0e38f && s->weight_offset < 3.0e38f)) return WUSH_ERR_INVALID_ARG;
@@ -231,45 +231,46 @@ int run(Args& a, bool vec, cudaStream_t st) {
 
 using namespace wush;
 
-extern "C" int wush_residual_norm(const void* y, int y_dtype, int64_t y_stride, const wush_norm_spec* post,
-                                  const void* gate, int gate_dtype, int64_t gate_stride, int gate_act, const void* r,
-                                  int r_dtype, int64_t r_stride, float residual_scale, float branch_scale, int64_t rows,
-                                  int64_t d, const wush_norm_spec* pre, void* r_out, int64_t r_out_stride, void* h,
-                                  int h_dtype, int64_t h_stride, void* stream) {
-  if (rows < 0 || d <= 0 || !y || (!r_out && !h)) return WUSH_ERR_INVALID_ARG;
+extern "C" int wush_residual_norm(const wush_residual_norm_args* args, void* stream) {
+  if (!args) return WUSH_ERR_INVALID_ARG;
+  const wush_residual_norm_args& q = *args;
+  const int64_t rows = q.rows, d = q.d;
+  if (rows < 0 || d <= 0 || !q.y || (!q.r_out && !q.h)) return WUSH_ERR_INVALID_ARG;
   if (d > kMaxWidth || rows > 0x7fffffff) return WUSH_ERR_UNSUPPORTED;
-  if (gate && (gate_act < WUSH_GATE_LINEAR || gate_act > WUSH_GATE_SILU)) return WUSH_ERR_UNSUPPORTED;
-  if (!(residual_scale - residual_scale == 0.0f) || !(branch_scale - branch_scale == 0.0f)) return WUSH_ERR_INVALID_ARG;
+  if (q.gate && (q.gate_act < WUSH_GATE_LINEAR || q.gate_act > WUSH_GATE_SILU)) return WUSH_ERR_UNSUPPORTED;
+  if (!(q.residual_scale - q.residual_scale == 0.0f) || !(q.branch_scale - q.branch_scale == 0.0f))
+    return WUSH_ERR_INVALID_ARG;
   bool vec = d % 8 == 0;
   Args a = {};
   int st;
-  if ((st = check_rows(y, y_dtype, y_stride, rows, d, false, &vec)) != WUSH_OK) return st;
-  if ((st = check_rows(gate, gate_dtype, gate_stride, rows, d, true, &vec)) != WUSH_OK) return st;
-  if ((st = check_rows(r, r_dtype, r_stride, rows, d, false, &vec)) != WUSH_OK) return st;
-  if ((st = check_rows(r_out, r_dtype, r_out_stride, rows, d, false, &vec)) != WUSH_OK) return st;
-  if ((st = check_rows(h, h_dtype, h_stride, rows, d, false, &vec)) != WUSH_OK) return st;
-  if ((st = check_norm(post, &a.post, &vec)) != WUSH_OK) return st;
-  if ((st = check_norm(pre, &a.pre, &vec)) != WUSH_OK) return st;
+  if ((st = check_rows(q.y, q.y_dtype, q.y_stride, rows, d, false, &vec)) != WUSH_OK) return st;
+  if ((st = check_rows(q.gate, q.gate_dtype, q.gate_stride, rows, d, true, &vec)) != WUSH_OK) return st;
+  if ((st = check_rows(q.r, q.r_dtype, q.r_stride, rows, d, false, &vec)) != WUSH_OK) return st;
+  if ((st = check_rows(q.r_out, q.r_dtype, q.r_out_stride, rows, d, false, &vec)) != WUSH_OK) return st;
+  if ((st = check_rows(q.h, q.h_dtype, q.h_stride, rows, d, false, &vec)) != WUSH_OK) return st;
+  if ((st = check_norm(&q.post, &a.post, &vec)) != WUSH_OK) return st;
+  if ((st = check_norm(&q.pre, &a.pre, &vec)) != WUSH_OK) return st;
   if (rows == 0) return WUSH_OK;
-  const Span sy = span(y, y_dtype, y_stride, d), sr = span(r, r_dtype, r_stride, d),
-             so = span(r_out, r_dtype, r_out_stride, d), sh = span(h, h_dtype, h_stride, d);
-  const bool in_place = r_out && r_out == r && r_out_stride == r_stride;
+  const Span sy = span(q.y, q.y_dtype, q.y_stride, d), sr = span(q.r, q.r_dtype, q.r_stride, d),
+             so = span(q.r_out, q.r_dtype, q.r_out_stride, d), sh = span(q.h, q.h_dtype, q.h_stride, d);
+  const bool in_place = q.r_out && q.r_out == q.r && q.r_out_stride == q.r_stride;
   if (overlap(so, sy, rows) || (!in_place && overlap(so, sr, rows)) || overlap(sh, sy, rows) ||
       overlap(sh, sr, rows) || overlap(sh, so, rows))
     return WUSH_ERR_INVALID_ARG;
   for (const Span& out : {so, sh}) {
+    if (!q.gate || !out.p) continue;
+    const char* g = static_cast<const char*>(q.gate);
     // (a gate per channel is one row, read by every row)
-    if (gate && gate_stride ? overlap(out, span(gate, gate_dtype, gate_stride, d), rows)
-                            : gate && out.p && out.p < static_cast<const char*>(gate) + d * dtype_bytes(gate_dtype) &&
-                                  static_cast<const char*>(gate) < out.p + (rows - 1) * out.stride + out.width)
+    if (q.gate_stride ? overlap(out, span(q.gate, q.gate_dtype, q.gate_stride, d), rows)
+                      : out.p < g + d * dtype_bytes(q.gate_dtype) && g < out.p + (rows - 1) * out.stride + out.width)
       return WUSH_ERR_INVALID_ARG;
   }
-  a.y = y; a.y_dt = y_dtype; a.y_stride = y_stride;
-  a.gate = gate; a.gate_dt = gate_dtype; a.gate_stride = gate_stride; a.act = gate_act;
-  a.r = r; a.r_dt = r_dtype; a.r_stride = r_stride;
-  a.r_out = r_out; a.r_out_stride = r_out_stride;
-  a.h = h; a.h_dt = h_dtype; a.h_stride = h_stride;
-  a.residual_scale = residual_scale; a.branch_scale = branch_scale;
+  a.y = q.y; a.y_dt = q.y_dtype; a.y_stride = q.y_stride;
+  a.gate = q.gate; a.gate_dt = q.gate_dtype; a.gate_stride = q.gate_stride; a.act = q.gate_act;
+  a.r = q.r; a.r_dt = q.r_dtype; a.r_stride = q.r_stride;
+  a.r_out = q.r_out; a.r_out_stride = q.r_out_stride;
+  a.h = q.h; a.h_dt = q.h_dtype; a.h_stride = q.h_stride;
+  a.residual_scale = q.residual_scale; a.branch_scale = q.branch_scale;
   a.rows = rows; a.d = static_cast<int>(d);
   return run(a, vec, static_cast<cudaStream_t>(stream));
 }

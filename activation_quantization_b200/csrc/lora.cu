@@ -22,7 +22,7 @@ namespace wush {
 namespace {
 
 constexpr int kMaxRank = 256;
-constexpr int64_t kMaxAdapters = 1 << 20;
+constexpr int64_t kMaxAdapters = 1 << 20, kMaxWidth = 1 << 24, kMaxTokens = 1 << 26;
 
 struct LoraArgs {
   const void* x;
@@ -308,33 +308,35 @@ extern "C" size_t wush_lora_workspace_bytes(int64_t tokens, int64_t d_in, int64_
   return 0;
 }
 
-extern "C" int wush_lora_add(const void* x, int x_dtype, int64_t x_stride, int64_t tokens, int64_t d_in,
-                             int64_t d_out, const int32_t* adapter, const void* a, const void* b,
-                             int64_t n_adapters, int64_t rank, const int32_t* ranks, const float* scale,
-                             const float* y_in, int64_t y_in_stride, float* y, int64_t y_stride, void* workspace,
-                             size_t workspace_bytes, void* stream) {
-  if (tokens < 0 || d_in <= 0 || d_in % 32 || d_out <= 0 || d_out % 8 || n_adapters <= 0 || rank <= 0 || rank % 8)
+extern "C" int wush_lora_add(const wush_lora_args* args, void* stream) {
+  if (!args) return WUSH_ERR_INVALID_ARG;
+  const wush_lora_args& q = *args;
+  if (q.tokens < 0 || q.d_in <= 0 || q.d_in % 32 || q.d_out <= 0 || q.d_out % 8 || q.n_adapters <= 0 || q.rank <= 0 ||
+      q.rank % 8)
     return WUSH_ERR_INVALID_ARG;
-  if (x_dtype != WUSH_BF16 && x_dtype != WUSH_FP16) return WUSH_ERR_UNSUPPORTED;
-  if (rank > kMaxRank || n_adapters > kMaxAdapters || d_in > (1 << 24) || d_out > (1 << 24) || tokens > (1 << 26))
+  if (q.dtype != WUSH_BF16 && q.dtype != WUSH_FP16) return WUSH_ERR_UNSUPPORTED;
+  if (q.rank > kMaxRank || q.n_adapters > kMaxAdapters || q.d_in > kMaxWidth || q.d_out > kMaxWidth ||
+      q.tokens > kMaxTokens)
     return WUSH_ERR_UNSUPPORTED;
-  if (tokens == 0) return WUSH_OK;
-  if (!x || !adapter || !a || !b || !y || !aligned16(x) || !aligned16(a) || !aligned16(b) || !aligned16(y) ||
-      (y_in && !aligned16(y_in)))
-    return WUSH_ERR_INVALID_ARG;
-  for (const void* p : {static_cast<const void*>(adapter), static_cast<const void*>(ranks), static_cast<const void*>(scale)})
+  if (q.tokens == 0) return WUSH_OK;
+  if (!q.x || !q.adapter || !q.a || !q.b || !q.y) return WUSH_ERR_INVALID_ARG;
+  for (const void* p : {q.x, q.a, q.b, static_cast<const void*>(q.y), static_cast<const void*>(q.y_in)})
+    if (!aligned16(p)) return WUSH_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(q.adapter), static_cast<const void*>(q.ranks),
+                        static_cast<const void*>(q.scale)})
     if (reinterpret_cast<uintptr_t>(p) & 3) return WUSH_ERR_INVALID_ARG;
-  if (x_stride < d_in || x_stride % 8 || y_stride < d_out || y_stride % 4) return WUSH_ERR_INVALID_ARG;
-  if (y_in && (y_in_stride < d_out || y_in_stride % 4)) return WUSH_ERR_INVALID_ARG;
-  const int64_t far = (int64_t(1) << 60) / tokens;
-  if (x_stride > far || y_stride > far || (y_in && y_in_stride > far)) return WUSH_ERR_UNSUPPORTED;
-  const Span out = span(y, WUSH_FP32, y_stride, d_out);
-  if (overlap(out, span(x, x_dtype, x_stride, d_in), tokens)) return WUSH_ERR_INVALID_ARG;
-  if (!(y == y_in && y_stride == y_in_stride) && overlap(out, span(y_in, WUSH_FP32, y_in_stride, d_out), tokens))
+  if (q.x_stride < q.d_in || q.x_stride % 8 || q.y_stride < q.d_out || q.y_stride % 4) return WUSH_ERR_INVALID_ARG;
+  if (q.y_in && (q.y_in_stride < q.d_out || q.y_in_stride % 4)) return WUSH_ERR_INVALID_ARG;
+  const int64_t far = (int64_t(1) << 60) / q.tokens;
+  if (q.x_stride > far || q.y_stride > far || (q.y_in && q.y_in_stride > far)) return WUSH_ERR_UNSUPPORTED;
+  const Span out = span(q.y, WUSH_FP32, q.y_stride, q.d_out);
+  if (overlap(out, span(q.x, q.dtype, q.x_stride, q.d_in), q.tokens)) return WUSH_ERR_INVALID_ARG;
+  if (!(q.y == q.y_in && q.y_stride == q.y_in_stride) &&
+      overlap(out, span(q.y_in, WUSH_FP32, q.y_in_stride, q.d_out), q.tokens))
     return WUSH_ERR_INVALID_ARG;
-  (void)workspace; (void)workspace_bytes;
-  LoraArgs p = {x, adapter, a, b, ranks, scale, y_in, y, x_stride, y_in_stride, y_stride, tokens,
-                static_cast<int>(d_in), static_cast<int>(d_out), static_cast<int>(n_adapters), static_cast<int>(rank)};
+  LoraArgs p = {q.x, q.adapter, q.a, q.b, q.ranks, q.scale, q.y_in, q.y, q.x_stride, q.y_in_stride, q.y_stride,
+                q.tokens, static_cast<int>(q.d_in), static_cast<int>(q.d_out), static_cast<int>(q.n_adapters),
+                static_cast<int>(q.rank)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return x_dtype == WUSH_FP16 ? run_lora<__half>(p, st) : run_lora<__nv_bfloat16>(p, st);
+  return q.dtype == WUSH_FP16 ? run_lora<__half>(p, st) : run_lora<__nv_bfloat16>(p, st);
 }

@@ -462,26 +462,34 @@ typedef struct {
 
 /* y:       device [rows, d] of y_dtype, row stride y_stride (in elements, as all
  *          strides here; >= d).
- * post:    N_post, or NULL for none.
  * gate:    device [rows, d] of gate_dtype with row stride gate_stride, or one row of
  *          d elements for all rows with gate_stride 0; act(g) is g, sigmoid(g) or
  *          g sigmoid(g) by gate_act.  NULL: no gate.
  * r:       device [rows, d] of r_dtype; NULL: no residual (r_out = branch_scale u).
  * r_out:   device [rows, d] of r_dtype; may be r itself (with r's stride).  NULL:
  *          not written.
- * pre, h:  N_pre (NULL for none) and its output, device [rows, d] of h_dtype.  h
- *          NULL: not computed.
+ * h:       N_pre(r_out), device [rows, d] of h_dtype.  NULL: not computed.
+ * post, pre: N_post and N_pre (kind NONE for none).
  * Requirements: 1 <= d <= 32768, 0 <= rows < 2^31 (0: nothing is launched), at least
  * one of r_out and h, finite scales, pointers aligned to their element; 16-byte
  * aligned rows and d % 8 == 0 run with 16-byte accesses.  Outputs may not overlap
  * each other or an input other than r_out = r (rows that interleave with equal
  * strides, i.e. columns of one wide buffer, do not overlap): WUSH_ERR_INVALID_ARG. */
-int wush_residual_norm(const void* y, int y_dtype, int64_t y_stride, const wush_norm_spec* post,
-                       const void* gate, int gate_dtype, int64_t gate_stride, int gate_act,
-                       const void* r, int r_dtype, int64_t r_stride, float residual_scale,
-                       float branch_scale, int64_t rows, int64_t d, const wush_norm_spec* pre,
-                       void* r_out, int64_t r_out_stride, void* h, int h_dtype, int64_t h_stride,
-                       void* stream);
+typedef struct {
+  const void* y;
+  const void* gate;
+  const void* r;
+  void* r_out;
+  void* h;
+  int64_t y_stride, gate_stride, r_stride, r_out_stride, h_stride;
+  int64_t rows, d;
+  wush_norm_spec post, pre;
+  int y_dtype, gate_dtype, r_dtype, h_dtype; /* wush_dtype */
+  int gate_act;                              /* wush_gate_act */
+  float residual_scale, branch_scale;
+} wush_residual_norm_args;
+
+int wush_residual_norm(const wush_residual_norm_args* args, void* stream);
 
 /* h = N(x): the norm before a block alone.  h may be x itself (same type and
  * stride).  Arguments and requirements as above. */
@@ -503,11 +511,11 @@ int wush_norm(const void* x, int x_dtype, int64_t x_stride, int64_t rows, int64_
  * A NaN or an infinity in a token's x or y_in reaches that token only, one in an
  * adapter that adapter's tokens only.
  *
- * x:        device [tokens, d_in], bf16 or fp16 (x_dtype), row stride x_stride (in
+ * x:        device [tokens, d_in], bf16 or fp16 (dtype), row stride x_stride (in
  *           elements, a multiple of 8).
  * adapter:  device int32 [tokens], in any order.
  * a, b:     device [n_adapters, rank, d_in] and [n_adapters, d_out, rank] of
- *           x_dtype: the two factors, each row contiguous.
+ *           dtype: the two factors, each row contiguous.
  * ranks:    device int32 [n_adapters]: k_g, clamped to [0, rank]; NULL: all rank.
  *           Rows of a and columns of b from k_g on are never used, whatever they hold.
  * scale:    device fp32 [n_adapters] or NULL (1).
@@ -519,13 +527,27 @@ int wush_norm(const void* x, int x_dtype, int64_t x_stride, int64_t rows, int64_
  *           two graphs) need one each.
  * Requirements: tokens >= 0 (0: nothing is launched), d_in % 32 == 0, d_out % 8 == 0,
  * rank % 8 == 0, 8 <= rank <= 256; WUSH_ERR_BUFFER_TOO_SMALL for a small workspace. */
+typedef struct {
+  const void* x;
+  const int32_t* adapter;
+  const void* a;
+  const void* b;
+  const int32_t* ranks;
+  const float* scale;
+  const float* y_in;
+  float* y;
+  void* workspace;
+  int64_t x_stride, y_in_stride, y_stride;
+  int64_t tokens, d_in, d_out, n_adapters, rank;
+  size_t workspace_bytes;
+  int dtype;                                 /* wush_dtype of x, a and b */
+} wush_lora_args;
+
+int wush_lora_add(const wush_lora_args* args, void* stream);
+
+/* Bytes of workspace for a call of these sizes (0 for sizes that are refused). */
 size_t wush_lora_workspace_bytes(int64_t tokens, int64_t d_in, int64_t d_out, int64_t n_adapters,
                                  int64_t rank);
-int wush_lora_add(const void* x, int x_dtype, int64_t x_stride, int64_t tokens, int64_t d_in,
-                  int64_t d_out, const int32_t* adapter, const void* a, const void* b,
-                  int64_t n_adapters, int64_t rank, const int32_t* ranks, const float* scale,
-                  const float* y_in, int64_t y_in_stride, float* y, int64_t y_stride, void* workspace,
-                  size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Diagnostics

@@ -1,7 +1,5 @@
 """What wush_norm and wush_residual_norm refuse, without a GPU: made-up pointers that are
 never dereferenced for the C calls, CPU tensors for the binding."""
-import ctypes
-
 import pytest
 
 aq = pytest.importorskip("activation_quantization_b200")
@@ -15,7 +13,7 @@ MB = 1 << 20
 
 
 def spec(kind=1, dtype=BF16, weight=64 * MB, bias=None, offset=0.0, eps=1e-6):
-    return aq._NormSpec(kind, dtype, weight, bias, offset, eps)
+    return kind, dtype, weight or 0, bias or 0, offset, eps
 
 
 def residual(**kw):
@@ -23,15 +21,16 @@ def residual(**kw):
     a = dict(y=1 * MB, yd=F32, ys=64, post=spec(), gate=2 * MB, gd=BF16, gs=64, act=1, r=3 * MB, rd=BF16, rs=64, a=1.0,
              b=1.0, rows=0, d=64, pre=spec(), o=4 * MB, os=64, h=5 * MB, hd=BF16, hs=64)
     a.update(kw)
-    ref = lambda s: None if s is None else ctypes.byref(s)  # noqa: E731
-    return lib.wush_residual_norm(a["y"], a["yd"], a["ys"], ref(a["post"]), a["gate"], a["gd"], a["gs"], a["act"],
-                                  a["r"], a["rd"], a["rs"], a["a"], a["b"], a["rows"], a["d"], ref(a["pre"]), a["o"],
-                                  a["os"], a["h"], a["hd"], a["hs"], None)
+    p = lambda k: a[k] or 0  # noqa: E731
+    return lib.wush_residual_norm(aq._RESIDUAL_NORM_ARGS.pack(
+        p("y"), p("gate"), p("r"), p("o"), p("h"), a["ys"], a["gs"], a["rs"], a["os"], a["hs"], a["rows"], a["d"],
+        *a["post"], *a["pre"], a["yd"], a["gd"], a["rd"], a["hd"], a["act"], a["a"], a["b"]), None)
 
 
 def test_residual_norm_refusals():
     assert residual() == OK
-    assert residual(post=None, pre=None, gate=None, r=None) == OK
+    assert lib.wush_residual_norm(None, None) == INVALID
+    assert residual(post=spec(kind=0), pre=spec(kind=0), gate=None, r=None) == OK
     assert residual(y=None) == INVALID and residual(o=None, h=None) == INVALID
     assert residual(o=None) == OK and residual(h=None) == OK
     assert residual(d=0) == INVALID and residual(rows=-1) == INVALID
@@ -81,7 +80,7 @@ def test_norm_refusals():
         a = dict(x=1 * MB, xd=F32, xs=64, rows=0, d=64, n=spec(), h=2 * MB, hd=F16, hs=64)
         a.update(kw)
         return lib.wush_norm(a["x"], a["xd"], a["xs"], a["rows"], a["d"],
-                             None if a["n"] is None else ctypes.byref(a["n"]), a["h"], a["hd"], a["hs"], None)
+                             None if a["n"] is None else aq._NORM_SPEC.pack(*a["n"]), a["h"], a["hd"], a["hs"], None)
 
     assert call() == OK and call(n=None) == INVALID and call(x=None) == INVALID and call(h=None) == INVALID
     assert call(d=0) == INVALID and call(rows=-3) == INVALID and call(d=1 << 16, xs=1 << 16, hs=1 << 16) == UNSUPPORTED

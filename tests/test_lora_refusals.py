@@ -16,13 +16,14 @@ def call(**kw):
     v = dict(x=1 * MB, xd=BF16, xs=256, tokens=1000, d_in=256, d_out=512, adapter=2 * MB, a=3 * MB, b=4 * MB, n=4,
              rank=16, ranks=5 * MB, scale=6 * MB, yi=16 * MB, yis=512, y=32 * MB, ys=512, ws=64 * MB, wn=1 << 40)
     v.update(kw)
-    return lib.wush_lora_add(v["x"], v["xd"], v["xs"], v["tokens"], v["d_in"], v["d_out"], v["adapter"], v["a"],
-                             v["b"], v["n"], v["rank"], v["ranks"], v["scale"], v["yi"], v["yis"], v["y"], v["ys"],
-                             v["ws"], v["wn"], None)
+    p = lambda k: v[k] or 0  # noqa: E731
+    return lib.wush_lora_add(aq._LORA_ARGS.pack(
+        p("x"), p("adapter"), p("a"), p("b"), p("ranks"), p("scale"), p("yi"), p("y"), p("ws"), v["xs"], v["yis"],
+        v["ys"], v["tokens"], v["d_in"], v["d_out"], v["n"], v["rank"], v["wn"], v["xd"]), None)
 
 
 def test_shapes_and_types():
-    assert call(tokens=0) == OK
+    assert call(tokens=0) == OK and lib.wush_lora_add(None, None) == INVALID
     assert call(tokens=-1) == INVALID
     for k, bad in (("d_in", (0, -32, 16, 48)), ("d_out", (0, 4, 12)), ("rank", (0, 4, 12, -8)), ("n", (0, -1))):
         for v in bad:
