@@ -5,9 +5,14 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace wush {
+
+// Error word of the kernels with bounded waits in block_norm.cu (see common.cuh).
+int read_and_clear_norm_error(int* word);
 
 inline int dtype_bytes(int dt) { return dt == WUSH_FP32 ? 4 : 2; }
 inline bool known_dtype(int dt) { return dt == WUSH_BF16 || dt == WUSH_FP32 || dt == WUSH_FP16; }
@@ -33,60 +38,101 @@ inline bool overlap(const Span& a, const Span& b, int64_t rows) {
   return delta < a.width || a.stride - delta < b.width;
 }
 
-// One element.
-__device__ __forceinline__ float load1(const void* p, int dt, int64_t i) {
-  if (dt == WUSH_FP32) return static_cast<const float*>(p)[i];
-  if (dt == WUSH_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  return __half2float(static_cast<const __half*>(p)[i]);
-}
-// (each output is rounded once, to nearest even; fp16 beyond its range becomes an infinity)
-__device__ __forceinline__ void store1(void* p, int dt, int64_t i, float v) {
-  if (dt == WUSH_FP32) static_cast<float*>(p)[i] = v;
-  else if (dt == WUSH_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-  else static_cast<__half*>(p)[i] = __float2half_rn(v);
+// Calls f with the element type as a compile-time constant, so that the branch lies
+// outside the loops of f.
+template <typename F>
+__device__ __forceinline__ void with_dtype(int dt, F f) {
+  if (dt == WUSH_BF16) f(std::integral_constant<int, WUSH_BF16>{});
+  else if (dt == WUSH_FP32) f(std::integral_constant<int, WUSH_FP32>{});
+  else f(std::integral_constant<int, WUSH_FP16>{});
 }
 
-// Eight consecutive elements from a 16-byte boundary.
-__device__ __forceinline__ void load8(const void* p, int dt, int64_t i, float (&v)[8]) {
-  if (dt == WUSH_FP32) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    return;
-  }
-  const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  if (dt == WUSH_BF16) {
+// Eight elements of a row as one thread of G holds them.  VEC: two quads, 4 G apart, so
+// that a warp's accesses are contiguous in every type (16 bytes a lane in fp32, 8 in
+// 16 bits); columns at or beyond d (a multiple of 4) read as zero.  Otherwise eight
+// single elements, G apart.
+template <bool VEC>
+__device__ __forceinline__ int group_column(int j, int e, int g, int tid) {
+  return VEC ? ((2 * j + (e >> 2)) * g + tid) * 4 + (e & 3) : (j * 8 + e) * g + tid;
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void load_group(const void* row, int j, int g, int tid, int d, float (&v)[8]) {
+  using T = typename std::conditional<DT == WUSH_FP32, float, uint16_t>::type;
+  const T* p = static_cast<const T*>(row);
+  auto convert = [](uint32_t u) {
+    return DT == WUSH_BF16 ? bf16_lo(u) : __half2float(__ushort_as_half(static_cast<unsigned short>(u)));
+  };
+  if (VEC) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) { v[2 * k] = bf16_lo(w[k]); v[2 * k + 1] = bf16_hi(w[k]); }
+    for (int h = 0; h < 2; ++h) {
+      const int c = group_column<true>(j, 4 * h, g, tid);
+      if (DT == WUSH_FP32) {
+        float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (c < d) q = *reinterpret_cast<const float4*>(p + c);
+        v[4 * h] = q.x; v[4 * h + 1] = q.y; v[4 * h + 2] = q.z; v[4 * h + 3] = q.w;
+      } else {
+        uint2 q = make_uint2(0u, 0u);
+        if (c < d) q = *reinterpret_cast<const uint2*>(p + c);
+        v[4 * h] = convert(q.x & 0xffffu); v[4 * h + 1] = convert(q.x >> 16);
+        v[4 * h + 2] = convert(q.y & 0xffffu); v[4 * h + 3] = convert(q.y >> 16);
+      }
+    }
   } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-      v[2 * k] = f.x; v[2 * k + 1] = f.y;
+    for (int e = 0; e < 8; ++e) {
+      const int c = group_column<false>(j, e, g, tid);
+      if (DT == WUSH_FP32) v[e] = c < d ? static_cast<const float*>(row)[c] : 0.0f;
+      else v[e] = convert(c < d ? static_cast<const uint16_t*>(row)[c] : 0u);
     }
   }
 }
-__device__ __forceinline__ void store8(void* p, int dt, int64_t i, const float (&v)[8]) {
-  if (dt == WUSH_FP32) {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
-    return;
-  }
-  uint32_t w[4];
+
+// Each element is rounded once, to nearest even (fp16 beyond its range becomes an
+// infinity).
+template <int DT, bool VEC>
+__device__ __forceinline__ void store_group(void* row, int j, int g, int tid, int d, const float (&v)[8]) {
+  uint32_t u[4];
+  if (DT != WUSH_FP32) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (dt == WUSH_BF16) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-      w[k] = *reinterpret_cast<const uint32_t*>(&b);
-    } else {
-      const __half2 b = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
-      w[k] = *reinterpret_cast<const uint32_t*>(&b);
+    for (int k = 0; k < 4; ++k) {
+      if (DT == WUSH_BF16) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+        u[k] = *reinterpret_cast<const uint32_t*>(&b);
+      } else {
+        const __half2 b = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+        u[k] = *reinterpret_cast<const uint32_t*>(&b);
+      }
     }
   }
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (VEC) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = group_column<true>(j, 4 * h, g, tid);
+      if (c >= d) continue;
+      if (DT == WUSH_FP32)
+        *reinterpret_cast<float4*>(static_cast<float*>(row) + c) =
+            make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(row) + c) = make_uint2(u[2 * h], u[2 * h + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = group_column<false>(j, e, g, tid);
+      if (c >= d) continue;
+      if (DT == WUSH_FP32) static_cast<float*>(row)[c] = v[e];
+      else static_cast<uint16_t*>(row)[c] = static_cast<uint16_t>(e & 1 ? u[e / 2] >> 16 : u[e / 2]);
+    }
+  }
+}
+
+// A row of a matrix of runtime type.
+__device__ __forceinline__ const void* row_of(const void* p, int dt, int64_t offset) {
+  return static_cast<const char*>(p) + offset * (dt == WUSH_FP32 ? 4 : 2);
+}
+__device__ __forceinline__ void* row_of(void* p, int dt, int64_t offset) {
+  return static_cast<char*>(p) + offset * (dt == WUSH_FP32 ? 4 : 2);
 }
 
 }  // namespace wush

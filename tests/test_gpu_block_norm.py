@@ -83,7 +83,8 @@ def check(lib, rows, d, y="fp32", r="bf16", h="bf16", w="bf16", post="rms", pre=
 
 @pytest.mark.parametrize("rows, d", [(1, 1), (1, 8), (3, 5), (2, 256), (9, 100), (5, 1000), (1, 4096), (299, 4096),
                                      (301, 1024), (700, 136), (2, 12288), (3, 8200), (1, 32768), (2, 32767),
-                                     (310, 4100), (4, 16392), (1531, 257)])
+                                     (310, 4100), (4, 16392), (1531, 257), (900, 40), (1000, 2048), (400, 8192), (333, 12288), (310, 20000),
+                                     (320, 32768), (305, 32767), (600, 6145)])
 @pytest.mark.parametrize("kind", ["rms", "layer"])
 def test_sizes(lib, rows, d, kind):
     check(lib, rows, d, post=kind, pre=kind, bias=kind == "layer", gate="element", act="silu")
