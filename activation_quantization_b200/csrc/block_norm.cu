@@ -76,7 +76,7 @@ struct Ring {
 
 __device__ __forceinline__ float activate(float g, int act) {
   if (act == WUSH_GATE_LINEAR) return g;
-  const float s = 1.0f / (1.0f + expf(-g));
+  const float s = __fdividef(1.0f, 1.0f + __expf(-g));     // (0 where the exponential overflows)
   return act == WUSH_GATE_SIGMOID ? s : g * s;
 }
 
@@ -101,10 +101,18 @@ __device__ __forceinline__ float row_sum(float s, float* red, int warps, int war
   return s;
 }
 
-// v = N(v) over the row; ``w`` and ``b`` are the vectors, wherever they lie.
+// A norm's vectors: in shared memory as fp32, the weight with its offset added
+// (``staged``), or where the caller has them.
+struct Vectors {
+  bool staged;
+  const float* w;
+  const float* b;
+};
+
+// v = N(v) over the row.
 template <bool VEC, int NV>
-__device__ __forceinline__ void apply_norm(const Args& a, const NormArgs& n, const void* w, const void* b,
-                                           float (&v)[NV][8], float (*red)[32], int g, int tid, int warp0, int d) {
+__device__ __forceinline__ void apply_norm(const Args& a, const NormArgs& n, const Vectors& vec, float (&v)[NV][8],
+                                           float (*red)[32], int g, int tid, int warp0, int d) {
   if (n.kind == WUSH_ROWNORM_NONE) return;
   const int warps = g >> 5;
   float s = 0.0f;
@@ -118,37 +126,49 @@ __device__ __forceinline__ void apply_norm(const Args& a, const NormArgs& n, con
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[j][e] = group_column<VEC>(j, e, g, tid) < d ? v[j][e] - mean : 0.0f;
-    s = 0.0f;
   }
+  float2 sq = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int j = 0; j < NV; ++j) sq = squares8(v[j], sq);
+  const float f = rsqrtf(fmaf(row_sum(sq.x + sq.y, red[1], warps, warp0), a.inv_d, n.eps));
+  if (vec.staged && vec.w) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(v[j][e], v[j][e], s);
-  const float f = rsqrtf(fmaf(row_sum(s, red[1], warps, warp0), a.inv_d, n.eps));
-  if (w) {
+    for (int j = 0; j < NV; ++j) {
+      float x[8];
+      load_group<WUSH_FP32, VEC>(vec.w, j, g, tid, d, x);
+      scale8(v[j], f);
+      mul8(v[j], x);
+    }
+  } else if (n.w) {
     with_dtype(n.dt, [&](auto dt) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float x[8];
-        load_group<dt.value, VEC>(w, j, g, tid, d, x);
+        load_group<dt.value, VEC>(n.w, j, g, tid, d, x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] = v[j][e] * f * (x[e] + n.offset);
+        for (int e = 0; e < 8; ++e) x[e] += n.offset;
+        scale8(v[j], f);
+        mul8(v[j], x);
       }
     });
   } else {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[j][e] *= f;
+    for (int j = 0; j < NV; ++j) scale8(v[j], f);
   }
-  if (b) {
+  if (vec.staged && vec.b) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float x[8];
+      load_group<WUSH_FP32, VEC>(vec.b, j, g, tid, d, x);
+      add8(v[j], x);
+    }
+  } else if (n.b) {
     with_dtype(n.dt, [&](auto dt) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float x[8];
-        load_group<dt.value, VEC>(b, j, g, tid, d, x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] += x[e];
+        load_group<dt.value, VEC>(n.b, j, g, tid, d, x);
+        add8(v[j], x);
       }
     });
   }
@@ -172,10 +192,10 @@ __device__ __forceinline__ void store_row(void* row, int dt, int g, int tid, int
 
 // v = residual_scale * r + branch_scale * v * act(gate)
 template <bool VEC, int NV>
-__device__ __forceinline__ void gate_and_add(const Args& a, const void* gate, const void* r, float (&v)[NV][8], int g,
+__device__ __forceinline__ void gate_and_add(const Args& a, const void* gate, int gate_dt, const void* r, float (&v)[NV][8], int g,
                                              int tid, int d) {
   if (gate)
-    with_dtype(a.gate_dt, [&](auto t) __attribute__((always_inline)) {
+    with_dtype(gate_dt, [&](auto t) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float x[8];
@@ -190,15 +210,12 @@ __device__ __forceinline__ void gate_and_add(const Args& a, const void* gate, co
       for (int j = 0; j < NV; ++j) {
         float x[8];
         load_group<t.value, VEC>(r, j, g, tid, d, x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] = fmaf(a.branch_scale, v[j][e], a.residual_scale * x[e]);
+        blend8(v[j], a.branch_scale, x, a.residual_scale);
       }
     });
   } else {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[j][e] *= a.branch_scale;
+    for (int j = 0; j < NV; ++j) scale8(v[j], a.branch_scale);
   }
 }
 
@@ -213,17 +230,20 @@ __global__ void __launch_bounds__(1024) norm_few_kernel(const __grid_constant__ 
   const bool live = row < a.rows;                          // the others only take part in the barriers
   const int d = live ? a.d : 0;
   float v[1][8];
+  sm100::pdl_wait();
+  sm100::pdl_launch_dependents();
   const void* r = a.r ? row_of(a.r, a.r_dt, row * a.r_stride) : nullptr;
   if (a.y) {
     load_row<VEC, 1>(row_of(a.y, a.y_dt, row * a.y_stride), a.y_dt, g, tid, d, v);
-    apply_norm<VEC, 1>(a, a.post, a.post.w, a.post.b, v, red, g, tid, warp0, d);
-    gate_and_add<VEC, 1>(a, a.gate ? row_of(a.gate, a.gate_dt, row * a.gate_stride) : nullptr, r, v, g, tid, d);
+    apply_norm<VEC, 1>(a, a.post, Vectors{}, v, red, g, tid, warp0, d);
+    gate_and_add<VEC, 1>(a, a.gate ? row_of(a.gate, a.gate_dt, row * a.gate_stride) : nullptr, a.gate_dt,
+                         r, v, g, tid, d);
     if (a.r_out) store_row<VEC, 1>(row_of(a.r_out, a.r_dt, row * a.r_out_stride), a.r_dt, g, tid, d, v);
   } else {
     load_row<VEC, 1>(r, a.r_dt, g, tid, d, v);
   }
   if (a.h) {
-    apply_norm<VEC, 1>(a, a.pre, a.pre.w, a.pre.b, v, red + 2, g, tid, warp0, d);
+    apply_norm<VEC, 1>(a, a.pre, Vectors{}, v, red + 2, g, tid, warp0, d);
     store_row<VEC, 1>(row_of(a.h, a.h_dt, row * a.h_stride), a.h_dt, g, tid, d, v);
   }
 }
@@ -237,8 +257,11 @@ __global__ void __launch_bounds__(1024) norm_few_kernel(const __grid_constant__ 
 // barrier of its own, r and the gate share one: y's stage is refilled as soon as the
 // first reduction has read it, the others' after the second.
 // ---------------------------------------------------------------------------
+// CTAs an SM: 64 registers a thread.
+constexpr int ring_ctas(int g) { return 1024 / g; }
+
 template <bool VEC, int NV, int G>
-__global__ void __launch_bounds__(G, 1024 / G) norm_ring_kernel(const __grid_constant__ Args a,
+__global__ void __launch_bounds__(G, ring_ctas(G)) norm_ring_kernel(const __grid_constant__ Args a,
                                                          const __grid_constant__ Ring q) {
   extern __shared__ __align__(128) char smem[];
   __shared__ __align__(16) float red[2][4][32];
@@ -247,7 +270,7 @@ __global__ void __launch_bounds__(G, 1024 / G) norm_ring_kernel(const __grid_con
   constexpr int g = G;                                     // (a constant, so that columns are immediate offsets)
   const int tid = threadIdx.x, d = a.d;
   const bool gate_rows = a.gate && a.gate_stride;
-  const int64_t n_rows = blockIdx.x < a.rows ? (a.rows - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+  const int n_rows = static_cast<int>((a.rows - 1 - blockIdx.x) / gridDim.x) + 1;   // (at most one CTA a row)
 
   if (tid == 0) {
     abort_flag = 0;
@@ -258,83 +281,81 @@ __global__ void __launch_bounds__(G, 1024 / G) norm_ring_kernel(const __grid_con
     sm100::fence_barrier_init();
   }
   for (int i = tid; i < 2 * 4 * 32; i += g) (&red[0][0][0])[i] = 0.0f;
-  // the vectors that every row uses
-  const void* vec[5] = {a.post.w, a.post.b, a.pre.w, a.pre.b, gate_rows ? nullptr : a.gate};
-  const int vec_dt[5] = {a.post.dt, a.post.dt, a.pre.dt, a.pre.dt, a.gate_dt};
-#pragma unroll
-  for (int k = 0; k < 5; ++k) {
-    if (!vec[k] || q.vec[k] < 0) continue;
-    if (vec_dt[k] == WUSH_FP32) {
-      for (int i = tid; i < d; i += g)
-        reinterpret_cast<uint32_t*>(smem + q.vec[k])[i] = static_cast<const uint32_t*>(vec[k])[i];
-    } else {
-      for (int i = tid; i < d; i += g)
-        reinterpret_cast<uint16_t*>(smem + q.vec[k])[i] = static_cast<const uint16_t*>(vec[k])[i];
-    }
-    vec[k] = smem + q.vec[k];
-  }
+  sm100::pdl_wait();                                       // nothing global is touched before this
+  sm100::pdl_launch_dependents();
+  // the vectors that every row uses, as fp32
+  auto stage = [&](const void* p, int dt, int at, float offset) -> const float* {
+    if (!p || at < 0) return nullptr;
+    float* out = reinterpret_cast<float*>(smem + at);
+    with_dtype(dt, [&](auto t) __attribute__((always_inline)) {
+      for (int i = tid; i < d; i += g) out[i] = load1<t.value>(p, i) + offset;
+    });
+    return out;
+  };
+  const Vectors post = {q.kept, stage(a.post.w, a.post.dt, q.vec[0], a.post.offset),
+                        stage(a.post.b, a.post.dt, q.vec[1], 0.0f)};
+  const Vectors pre = {q.kept, stage(a.pre.w, a.pre.dt, q.vec[2], a.pre.offset),
+                       stage(a.pre.b, a.pre.dt, q.vec[3], 0.0f)};
+  const float* gate_vec = gate_rows ? nullptr : stage(a.gate, a.gate_dt, q.vec[4], 0.0f);
   __syncthreads();
 
-  // One row of one tensor into its stage: its whole 16-byte units (bytes returned, issued
-  // by thread 0) and, by the first threads, the elements at its ends.
-  auto units = [&](const char* src, int size, int64_t* lo) {
-    const int64_t at = reinterpret_cast<int64_t>(src);
+  // One row of one tensor into its stage: its whole 16-byte units by a bulk copy (thread 0;
+  // ``units`` gives their first byte and their number of bytes) and, by the first warp, the
+  // elements at its ends.
+  auto units = [&](int64_t at, int size, int64_t* lo) {
+    const int64_t end = at + int64_t(d) * size, hi = VEC ? end : end & ~int64_t(15);
     *lo = VEC ? at : (at + 15) & ~int64_t(15);
-    const int64_t hi = VEC ? at + int64_t(d) * size : (at + int64_t(d) * size) & ~int64_t(15);
     return hi > *lo ? static_cast<uint32_t>(hi - *lo) : 0u;
   };
-  auto ends = [&](const char* src, int size, char* stage) {
-    if (VEC || tid >= 32) return;
+  auto bulk = [&](int64_t at, int size, char* to, uint64_t* bar) {
     int64_t lo;
-    const int64_t bytes = units(src, size, &lo), at = reinterpret_cast<int64_t>(src);
-    const int head = bytes ? static_cast<int>(lo - at) / size : d;        // elements before the units
+    const uint32_t bytes = units(at, size, &lo);
+    if (bytes) sm100::bulk_load(to + (at & 15) + (lo - at), reinterpret_cast<const void*>(lo), bytes, bar);
+  };
+  auto ends = [&](int64_t at, int size, char* to) {
+    int64_t lo;
+    const uint32_t bytes = units(at, size, &lo);
+    const int head = bytes ? static_cast<int>(lo - at) / size : d;          // elements before the units
     const int tail = bytes ? static_cast<int>(lo + bytes - at) / size : d;  // first element behind them
     for (int i = tid; i < head + (d - tail); i += 32) {
-      const int64_t e = int64_t(i < head ? i : tail + i - head) * size;
-      char* dst = stage + (at & 15) + e;
-      if (size == 4) *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src + e);
-      else *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src + e);
+      const int e = (i < head ? i : tail + i - head) * size;
+      char* dst = to + (at & 15) + e;
+      if (size == 4) *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(at + e);
+      else *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(at + e);
     }
   };
-  auto source = [&](const void* p, int dt, int64_t stride, int64_t i) {
-    return static_cast<const char*>(row_of(p, dt, (blockIdx.x + i * gridDim.x) * stride));
+  auto address = [&](const void* p, int dt, int64_t stride, int i) {       // of the CTA's row i
+    return reinterpret_cast<int64_t>(row_of(p, dt, (blockIdx.x + int64_t(i) * gridDim.x) * stride));
   };
-  auto bulk = [&](const char* src, int size, char* stage, uint64_t* bar) {
-    int64_t lo;
-    const uint32_t bytes = units(src, size, &lo);
-    if (bytes) sm100::bulk_load(stage + (reinterpret_cast<int64_t>(src) & 15) + (lo - reinterpret_cast<int64_t>(src)),
-                                reinterpret_cast<const void*>(lo), bytes, bar);
-  };
-  auto fill_y = [&](int64_t i) {                           // the CTA's row i
-    if (!a.y || i >= n_rows) return;
-    const int s = static_cast<int>(i % q.stages), size = a.y_dt == WUSH_FP32 ? 4 : 2;
-    const char* src = source(a.y, a.y_dt, a.y_stride, i);
-    char* stage = smem + q.y + s * q.y_step;
+  const bool r_ring = a.r && q.r >= 0, gate_ring = gate_rows && q.gate >= 0;
+  const int y_size = a.y_dt == WUSH_FP32 ? 4 : 2, r_size = a.r_dt == WUSH_FP32 ? 4 : 2,
+            gate_size = a.gate_dt == WUSH_FP32 ? 4 : 2;
+  auto fill_y = [&](int i, int s) {                        // the CTA's row i into stage s
+    if (!a.y || i >= n_rows || tid >= (VEC ? 1 : 32)) return;
+    const int64_t at = address(a.y, a.y_dt, a.y_stride, i);
+    char* to = smem + q.y + s * q.y_step;
     if (tid == 0) {
       int64_t lo;
-      sm100::mbar_arrive_expect_tx(&full[0][s], units(src, size, &lo));
-      bulk(src, size, stage, &full[0][s]);
+      sm100::mbar_arrive_expect_tx(&full[0][s], units(at, y_size, &lo));
+      bulk(at, y_size, to, &full[0][s]);
     }
-    ends(src, size, stage);
+    if (!VEC) ends(at, y_size, to);
   };
-  auto fill_rest = [&](int64_t i) {
-    if (i >= n_rows) return;
-    const int s = static_cast<int>(i % q.stages);
-    const int r_size = a.r_dt == WUSH_FP32 ? 4 : 2, g_size = a.gate_dt == WUSH_FP32 ? 4 : 2;
-    const bool with_r = a.r && q.r >= 0, with_g = gate_rows && q.gate >= 0;
-    const char* src_r = with_r ? source(a.r, a.r_dt, a.r_stride, i) : nullptr;
-    const char* src_g = with_g ? source(a.gate, a.gate_dt, a.gate_stride, i) : nullptr;
-    char* stage_r = smem + q.r + s * q.r_step;
-    char* stage_g = smem + q.gate + s * q.gate_step;
+  auto fill_rest = [&](int i, int s) {
+    if (i >= n_rows || tid >= (VEC ? 1 : 32)) return;
+    const int64_t at_r = r_ring ? address(a.r, a.r_dt, a.r_stride, i) : 0;
+    const int64_t at_g = gate_ring ? address(a.gate, a.gate_dt, a.gate_stride, i) : 0;
+    char* to_r = smem + q.r + s * q.r_step;
+    char* to_g = smem + q.gate + s * q.gate_step;
     if (tid == 0) {
       int64_t lo;
-      sm100::mbar_arrive_expect_tx(&full[1][s], (with_r ? units(src_r, r_size, &lo) : 0u) +
-                                                    (with_g ? units(src_g, g_size, &lo) : 0u));
-      if (with_r) bulk(src_r, r_size, stage_r, &full[1][s]);
-      if (with_g) bulk(src_g, g_size, stage_g, &full[1][s]);
+      sm100::mbar_arrive_expect_tx(&full[1][s], (r_ring ? units(at_r, r_size, &lo) : 0u) +
+                                                    (gate_ring ? units(at_g, gate_size, &lo) : 0u));
+      if (r_ring) bulk(at_r, r_size, to_r, &full[1][s]);
+      if (gate_ring) bulk(at_g, gate_size, to_g, &full[1][s]);
     }
-    if (with_r) ends(src_r, r_size, stage_r);
-    if (with_g) ends(src_g, g_size, stage_g);
+    if (!VEC && r_ring) ends(at_r, r_size, to_r);
+    if (!VEC && gate_ring) ends(at_g, gate_size, to_g);
   };
   // (a wait that gives up marks the error and lets the CTA run on, so that its barriers
   // stay uniform; every later wait then gives up at once)
@@ -346,44 +367,46 @@ __global__ void __launch_bounds__(G, 1024 / G) norm_ring_kernel(const __grid_con
     }
   };
 
-  for (int64_t i = 0; i < q.stages; ++i) {
-    fill_y(i);
-    fill_rest(i);
+  for (int i = 0; i < q.stages; ++i) {
+    fill_y(i, i);
+    fill_rest(i, i);
   }
-  for (int64_t i = 0; i < n_rows; ++i) {
-    const int s = static_cast<int>(i % q.stages);
-    const uint32_t parity = static_cast<uint32_t>(i / q.stages) & 1u;
-    const int64_t row = blockIdx.x + i * gridDim.x;
+  int s = 0;
+  uint32_t parity = 0;
+  for (int i = 0; i < n_rows; ++i) {
+    const int64_t row = blockIdx.x + int64_t(i) * gridDim.x;
     float (*sums)[32] = red[i & 1];
     float v[NV][8];
+    // a row lies in its stage at the 16-byte phase that it has in global memory
     auto phase = [&](const void* p, int dt, int64_t stride) {
       return VEC ? 0 : static_cast<int>(reinterpret_cast<int64_t>(row_of(p, dt, row * stride)) & 15);
     };
-    auto r_row = [&]() -> const void* {
-      return q.r >= 0 ? smem + q.r + s * q.r_step + phase(a.r, a.r_dt, a.r_stride)
-                      : row_of(a.r, a.r_dt, row * a.r_stride);
-    };
+    const char* r_stage = smem + q.r + s * q.r_step + phase(a.r, a.r_dt, a.r_stride);
     if (!VEC) __syncthreads();                             // the rows' ends are in place
     if (a.y) {
       wait(&full[0][s], parity);
       load_row<VEC, NV>(smem + q.y + s * q.y_step + phase(a.y, a.y_dt, a.y_stride), a.y_dt, g, tid, d, v);
-      apply_norm<VEC, NV>(a, a.post, vec[0], vec[1], v, sums, g, tid, 0, d);
+      apply_norm<VEC, NV>(a, a.post, post, v, sums, g, tid, 0, d);
       if (a.post.kind == WUSH_ROWNORM_NONE) __syncthreads();
-      fill_y(i + q.stages);
+      fill_y(i + q.stages, s);
       wait(&full[1][s], parity);
-      const void* gate = !gate_rows ? vec[4]
-                         : q.gate >= 0 ? smem + q.gate + s * q.gate_step + phase(a.gate, a.gate_dt, a.gate_stride)
-                                       : row_of(a.gate, a.gate_dt, row * a.gate_stride);
-      gate_and_add<VEC, NV>(a, gate, a.r ? r_row() : nullptr, v, g, tid, d);
+      const void* gate = nullptr;
+      int gate_dt = a.gate_dt;
+      if (gate_ring) gate = smem + q.gate + s * q.gate_step + phase(a.gate, a.gate_dt, a.gate_stride);
+      else if (gate_vec) gate = gate_vec, gate_dt = WUSH_FP32;
+      else if (a.gate) gate = row_of(a.gate, a.gate_dt, row * a.gate_stride);
+      gate_and_add<VEC, NV>(a, gate, gate_dt,
+                            r_ring ? r_stage : a.r ? row_of(a.r, a.r_dt, row * a.r_stride) : nullptr, v, g, tid, d);
       if (a.r_out) store_row<VEC, NV>(row_of(a.r_out, a.r_dt, row * a.r_out_stride), a.r_dt, g, tid, d, v);
     } else {
       wait(&full[1][s], parity);
-      load_row<VEC, NV>(r_row(), a.r_dt, g, tid, d, v);
+      load_row<VEC, NV>(r_stage, a.r_dt, g, tid, d, v);
     }
-    if (a.h) apply_norm<VEC, NV>(a, a.pre, vec[2], vec[3], v, sums + 2, g, tid, 0, d);
+    if (a.h) apply_norm<VEC, NV>(a, a.pre, pre, v, sums + 2, g, tid, 0, d);
     if (!a.h || a.pre.kind == WUSH_ROWNORM_NONE) __syncthreads();
-    fill_rest(i + q.stages);
+    fill_rest(i + q.stages, s);
     if (a.h) store_row<VEC, NV>(row_of(a.h, a.h_dt, row * a.h_stride), a.h_dt, g, tid, d, v);
+    if (++s == q.stages) s = 0, parity ^= 1;
   }
   if (gave_up) {
     atomicOr(&g_norm_error, kErrTimeoutBarrier);
@@ -426,10 +449,17 @@ int check_rows(const void* p, int dt, int64_t stride, int64_t rows, int64_t d, b
 
 constexpr int kSmemPerSm = 224 * 1024;                     // what the rings of an SM's CTAs share
 constexpr int kCtaOverhead = 3 * 1024;                     // static and reserved shared memory of a CTA
+constexpr int kInFlight = 96 * 1024;                       // bytes of rows that an SM asks for ahead
 
-// The ring kernel's layout for ``ctas`` CTAs an SM: the shared memory it takes, or 0
-// where not even one stage of y (or, without y, of x) fits.
-int plan(const Args& a, bool vec, int ctas, int want_stages, Ring* q) {
+// The ring kernel's layout for ``ctas`` CTAs an SM, and the shared memory it takes.
+//
+// An SM needs some 50 KB in flight to fill its share of the memory's bandwidth; with as
+// many CTAs as the registers allow, one stage each gives that for rows of 24 KB (a stage
+// is refilled while its row is still being worked on in registers) and narrower rows take
+// up to four.  Measured at 4096 rows x 4096 (fp32 y, bf16 stream): four CTAs of 256
+// threads with one stage 30.7 us, two with two stages 34.4 us, eight of 128 threads 32.5 us;
+// at 8192 x 5120 bf16: 32.1 us with two stages, 36.6 us with one.
+int plan(const Args& a, bool vec, int ctas, Ring* q) {
   const int budget = kSmemPerSm / ctas - kCtaOverhead;
   auto up = [](int64_t n) { return static_cast<int>((n + 15) / 16 * 16); };
   const bool gate_rows = a.gate && a.gate_stride;
@@ -437,62 +467,49 @@ int plan(const Args& a, bool vec, int ctas, int want_stages, Ring* q) {
   const int y = a.y ? up(int64_t(a.d) * dtype_bytes(a.y_dt) + edge) : 0;
   int r = a.r ? up(int64_t(a.d) * dtype_bytes(a.r_dt) + edge) : 0;
   int gate = gate_rows ? up(int64_t(a.d) * dtype_bytes(a.gate_dt) + edge) : 0;
-  if (gate && y + r + gate > budget) gate = 0;             // rows too wide: read where they lie
+  if (gate && y + r + gate > budget) gate = 0;             // too wide: read where it lies
   if (y && y + r + gate > budget) r = 0;
-  if (y + r + gate > budget) return 0;
-  const void* vecs[5] = {a.post.w, a.post.b, a.pre.w, a.pre.b, gate_rows ? nullptr : a.gate};
-  const int dts[5] = {a.post.dt, a.post.dt, a.pre.dt, a.pre.dt, a.gate_dt};
-  int all = 0;
-  for (int k = 0; k < 5; ++k) all += vecs[k] ? up(int64_t(a.d) * dtype_bytes(dts[k])) : 0;
-  const int stage = y + r + gate > 0 ? y + r + gate : 16;
-  // vectors that leave no room for the stages stay where they are (in L2)
-  const bool keep = q->kept = all + want_stages * stage <= budget;
-  q->stages = (budget - (keep ? all : 0)) / stage;
+  const int stage = y + r + gate > 16 ? y + r + gate : 16;
+  q->stages = kInFlight / ctas / stage;
+  if (q->stages < 1) q->stages = 1;
   if (q->stages > kMaxStages) q->stages = kMaxStages;
+  const void* vecs[5] = {a.post.w, a.post.b, a.pre.w, a.pre.b, gate_rows ? nullptr : a.gate};
+  int all = 0;
+  for (int k = 0; k < 5; ++k) all += vecs[k] ? up(int64_t(a.d) * 4) : 0;
+  q->kept = all + q->stages * stage <= budget;             // otherwise they are read from L2, row by row
   int at = 0;
   q->y = at; q->y_step = y; at += y * q->stages;
   q->r = r ? at : -1; q->r_step = r; at += r * q->stages;
   q->gate = gate ? at : -1; q->gate_step = gate; at += gate * q->stages;
   for (int k = 0; k < 5; ++k) {
-    q->vec[k] = keep && vecs[k] ? at : -1;
-    if (q->vec[k] >= 0) at += up(int64_t(a.d) * dtype_bytes(dts[k]));
+    q->vec[k] = q->kept && vecs[k] ? at : -1;
+    if (q->vec[k] >= 0) at += up(int64_t(a.d) * 4);
   }
-  return at > 16 ? at : 16;
+  return at;
 }
 
 template <bool VEC, int NV, int G>
 int launch_ring(const Args& a, int sms, cudaStream_t st) {
   Ring q = {};
-  // As many CTAs an SM as leave each two stages and the vectors (while one CTA waits in
-  // its reductions the others use the memory); where rows are too wide for that, two
-  // stages without the vectors, then what fits.
-  constexpr int kMost = 1024 / G;                          // (64 registers a thread)
-  int ctas = kMost, smem = 0;
-  while (ctas > 0 && !((smem = plan(a, VEC, ctas, 2, &q)) && q.kept && q.stages >= 2)) --ctas;
-  if (ctas == 0)
-    for (ctas = kMost; ctas > 1 && !((smem = plan(a, VEC, ctas, 2, &q)) && q.stages >= 2);) --ctas;
-  if (ctas == 1) smem = plan(a, VEC, 1, q.kept && q.stages >= 2 ? 2 : 1, &q);
-  if (!smem) return WUSH_ERR_UNSUPPORTED;
+  const int ctas = ring_ctas(G), smem = plan(a, VEC, ctas, &q);
   auto kern = norm_ring_kernel<VEC, NV, G>;
   static std::atomic<uint64_t> done{0};
   if (set_smem_once(kern, kSmemPerSm, done) != WUSH_OK) return WUSH_ERR_CUDA;
   const int64_t grid = int64_t(ctas) * sms < a.rows ? int64_t(ctas) * sms : a.rows;
-  kern<<<static_cast<unsigned>(grid), G, smem, st>>>(a, q);
-  return launch_status();
+  return launch_pdl(kern, static_cast<unsigned>(grid), G, smem, st, a, q);
 }
 
-// Threads of a row and elements of a thread: up to 32 elements, and as few threads as
-// hold the row then, since a reduction's cost grows with its warps.
+// Threads of a row: 256 with up to 32 elements each; fewer for narrow rows, more for wide
+// ones.
 template <bool VEC>
 int launch_width(const Args& a, int sms, cudaStream_t st) {
-  const int per128 = (a.d + 1023) / 1024;
-  if (per128 == 1) return launch_ring<VEC, 1, 128>(a, sms, st);
-  if (per128 == 2) return launch_ring<VEC, 2, 128>(a, sms, st);
-  if (per128 <= 4) return launch_ring<VEC, 2, 256>(a, sms, st);
-  if (per128 <= 6) return launch_ring<VEC, 3, 256>(a, sms, st);
-  if (per128 <= 8) return launch_ring<VEC, 4, 256>(a, sms, st);
-  if (per128 <= 12) return launch_ring<VEC, 3, 512>(a, sms, st);
-  if (per128 <= 16) return launch_ring<VEC, 4, 512>(a, sms, st);
+  if (a.d <= 1024) return launch_ring<VEC, 1, 128>(a, sms, st);
+  if (a.d <= 2048) return launch_ring<VEC, 1, 256>(a, sms, st);
+  if (a.d <= 4096) return launch_ring<VEC, 2, 256>(a, sms, st);
+  if (a.d <= 6144) return launch_ring<VEC, 3, 256>(a, sms, st);
+  if (a.d <= 8192) return launch_ring<VEC, 4, 256>(a, sms, st);
+  if (a.d <= 12288) return launch_ring<VEC, 3, 512>(a, sms, st);
+  if (a.d <= 16384) return launch_ring<VEC, 4, 512>(a, sms, st);
   return launch_ring<VEC, 4, 1024>(a, sms, st);
 }
 
@@ -512,9 +529,8 @@ int run(Args& a, bool vec, cudaStream_t st) {
     a.row_threads = threads;
     const int block = threads < kMinThreads ? kMinThreads : threads;
     const int64_t per = block / threads, grid = (a.rows + per - 1) / per;
-    if (vec) norm_few_kernel<true><<<static_cast<unsigned>(grid), block, 0, st>>>(a);
-    else norm_few_kernel<false><<<static_cast<unsigned>(grid), block, 0, st>>>(a);
-    return launch_status();
+    return vec ? launch_pdl(norm_few_kernel<true>, static_cast<unsigned>(grid), block, 0, st, a)
+               : launch_pdl(norm_few_kernel<false>, static_cast<unsigned>(grid), block, 0, st, a);
   }
   return vec ? launch_width<true>(a, sms, st) : launch_width<false>(a, sms, st);
 }

@@ -17,6 +17,26 @@ int read_and_clear_norm_error(int* word);
 inline int dtype_bytes(int dt) { return dt == WUSH_FP32 ? 4 : 2; }
 inline bool known_dtype(int dt) { return dt == WUSH_BF16 || dt == WUSH_FP32 || dt == WUSH_FP16; }
 
+// Launches with programmatic stream serialization: the kernel may be set up while the one
+// before it ends, and waits for it (pdl_wait) before it touches global memory.  It lets its
+// own dependents start (pdl_launch_dependents) only after that wait, so that whatever a
+// dependent reads before its own wait is already complete.
+template <typename... P, typename... A>
+inline int launch_pdl(void (*kern)(P...), unsigned grid, int block, int smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(static_cast<unsigned>(block));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return WUSH_ERR_CUDA;
+  return launch_status();
+}
+
 struct Span {                                              // rows of a tensor, as bytes
   const char* p;
   int64_t stride, width;                                   // bytes
@@ -45,6 +65,54 @@ __device__ __forceinline__ void with_dtype(int dt, F f) {
   if (dt == WUSH_BF16) f(std::integral_constant<int, WUSH_BF16>{});
   else if (dt == WUSH_FP32) f(std::integral_constant<int, WUSH_FP32>{});
   else f(std::integral_constant<int, WUSH_FP16>{});
+}
+
+// Two fp32 values at a time (sm_100's packed FMA pipe).
+__device__ __forceinline__ void mul8(float (&v)[8], const float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float2 p = __fmul2_rn(make_float2(v[e], v[e + 1]), make_float2(x[e], x[e + 1]));
+    v[e] = p.x; v[e + 1] = p.y;
+  }
+}
+__device__ __forceinline__ void scale8(float (&v)[8], float f) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float2 p = __fmul2_rn(make_float2(v[e], v[e + 1]), make_float2(f, f));
+    v[e] = p.x; v[e + 1] = p.y;
+  }
+}
+__device__ __forceinline__ void add8(float (&v)[8], const float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float2 p = __fadd2_rn(make_float2(v[e], v[e + 1]), make_float2(x[e], x[e + 1]));
+    v[e] = p.x; v[e + 1] = p.y;
+  }
+}
+// v = f * v + g * x
+__device__ __forceinline__ void blend8(float (&v)[8], float f, const float (&x)[8], float g) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float2 q = __fmul2_rn(make_float2(x[e], x[e + 1]), make_float2(g, g));
+    const float2 p = __ffma2_rn(make_float2(v[e], v[e + 1]), make_float2(f, f), q);
+    v[e] = p.x; v[e + 1] = p.y;
+  }
+}
+__device__ __forceinline__ float2 squares8(const float (&v)[8], float2 s) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float2 p = make_float2(v[e], v[e + 1]);
+    s = __ffma2_rn(p, p, s);
+  }
+  return s;
+}
+
+// One element.
+template <int DT>
+__device__ __forceinline__ float load1(const void* p, int64_t i) {
+  if (DT == WUSH_FP32) return static_cast<const float*>(p)[i];
+  if (DT == WUSH_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
 }
 
 // Eight elements of a row as one thread of G holds them.  VEC: two quads, 4 G apart, so

@@ -71,8 +71,10 @@ def check(lib, rows, d, y="fp32", r="bf16", h="bf16", w="bf16", post="rms", pre=
     u, o, hh = B.residual_norm(y64, r64, post, pw, pb, g64, act, a, b, pre, qw, qb, eps, offset)
     e = norm_error(y64, np.zeros_like(y64), post, pw, pb, eps, offset)
     if g64 is not None:
-        # expf is within 2 ulp, the quotient and two products round once each
-        e = e * np.abs(B.activate(g64, act)) + 8 * U * np.abs(u)
+        # exp(-g) is 2^t with t = fp32(-g log2 e): t is off by u |g| log2 e, which is u |g| of the
+        # exponential, and 2^t by 2 ulp (4 u); the sum rounds once, the quotient is within 2 ulp (4 u) and
+        # two products round once each
+        e = e * np.abs(B.activate(g64, act)) + (11 + np.abs(g64)) * U * np.abs(u)
     e = abs(b) * e + 3 * U * (np.abs(b * u) + (0 if r64 is None else np.abs(a * r64)))
     if want_r:
         close(out, o, r, e)
