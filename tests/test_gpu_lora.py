@@ -202,3 +202,8 @@ def test_sizes_of_the_listed_projections(lib):
     check(lib, 16, 4096, 4096, 4, 64, HF, ranks=[64, 32, 16, 61])
     check(lib, 260, 5120, 17408, 3, 16)
     check(lib, 300, 12288, 4096, 3, 64)
+
+
+def test_a_pool_too_large_to_count_in_shared_memory(lib):
+    assert lib.wush_lora_workspace_bytes(150, 64, 64, 20000, 8) == 0
+    check(lib, 150, 64, 64, 20000, 8, adapter=torch.cat([torch.randperm(20000)[:100], torch.full((50,), 19999)]))
