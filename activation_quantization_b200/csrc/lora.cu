@@ -42,12 +42,12 @@ template <typename E>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   if constexpr (std::is_same<E, __half>::value)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -548,22 +548,27 @@ __global__ void __launch_bounds__(kShrinkThreads, NB <= 8 ? 3 : 1) lora_shrink_k
     cp_async_commit();
     if (active) {
       const uint32_t at = base + (step - first) % kShrinkStages * kStage;
+      // FULL: every block of 8 ranks is in use, so that the loads need not wait for tests
+      auto multiply = [&](auto full) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < kBk / 32; ++i) {
-        const int ks = wk * (kBk / 32) + i;
-        uint32_t a[4];
-        const int ar = wm * 16 + (lane & 15);
-        ldmatrix4(at + ar * 128 + (((2 * ks + (lane >> 4)) ^ (ar & 7)) << 4), a);
+        for (int i = 0; i < kBk / 32; ++i) {
+          const int ks = wk * (kBk / 32) + i;
+          uint32_t a[4];
+          const int ar = wm * 16 + (lane & 15);
+          ldmatrix4(at + ar * 128 + (((2 * ks + (lane >> 4)) ^ (ar & 7)) << 4), a);
 #pragma unroll
-        for (int b = 0; b < NB; b += 2) {
-          if (b * 8 >= k) break;
-          uint32_t q[4];
-          const int br = b * 8 + (lane & 7) + ((lane >> 4) << 3);
-          ldmatrix4(at + (kTile + br) * 128 + (((2 * ks + ((lane >> 3) & 1)) ^ (br & 7)) << 4), q);
-          mma16816<E>(acc[b], a[0], a[1], a[2], a[3], q[0], q[1]);
-          mma16816<E>(acc[b + 1], a[0], a[1], a[2], a[3], q[2], q[3]);
+          for (int b = 0; b < NB; b += 2) {
+            if (!full.value && b * 8 >= k) break;
+            uint32_t q[4];
+            const int br = b * 8 + (lane & 7) + ((lane >> 4) << 3);
+            ldmatrix4(at + (kTile + br) * 128 + (((2 * ks + ((lane >> 3) & 1)) ^ (br & 7)) << 4), q);
+            mma16816<E>(acc[b], a[0], a[1], a[2], a[3], q[0], q[1]);
+            mma16816<E>(acc[b + 1], a[0], a[1], a[2], a[3], q[2], q[3]);
+          }
         }
-      }
+      };
+      if (k > (NB - 2) * 8) multiply(std::true_type{});
+      else multiply(std::false_type{});
     }
     if ((step - first) % 16 == 15) {
       flush_all(fresh);
@@ -620,11 +625,13 @@ __global__ void __launch_bounds__(kShrinkThreads, NB <= 8 ? 3 : 1) lora_shrink_k
 // values of both blocks are four consecutive columns: one 16-byte access of y each.  y_in
 // goes into slots that only the thread itself reads.  Rows of B and of the terms are 16
 // bytes longer than the ranks, which spreads a fragment's rows over the banks.
-template <typename E>
+// KS: the rank's MMA steps that have an unrolled loop.
+template <typename E, int KS>
 __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const __grid_constant__ LoraArgs p,
-                                                                     const __grid_constant__ Work w, int row_bytes,
-                                                                     int stages, int run) {
+                                                                     const __grid_constant__ Work w, int stages,
+                                                                     int most_run) {
   constexpr int kT = Split<E>::kTerms;
+  const int row_bytes = w.row_elems * 2 + 16;
   extern __shared__ __align__(128) unsigned char smem[];   // terms [kT][kTile] rows; per stage: y_in slots, B rows
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int wm = warp & 3, wn = warp >> 2, g = lane >> 2, c = lane & 3;
@@ -633,8 +640,12 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const __gri
   const uint32_t s_base = sm100::smem_u32(smem), ring = s_base + kT * kTile * row_bytes;
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
-  const int blocks = (p.d_out + kCols - 1) / kCols, runs = (blocks + run - 1) / run;
-  const int64_t items = static_cast<int64_t>(*w.n_tiles) * runs;
+  // a run of column blocks as long as still gives every CTA a few items
+  const int blocks = (p.d_out + kCols - 1) / kCols, n_tiles = *w.n_tiles;
+  int run = static_cast<int>(static_cast<int64_t>(n_tiles) * blocks / (4 * gridDim.x));
+  run = run < 2 ? 2 : run > most_run ? most_run : run;
+  const int runs = (blocks + run - 1) / run;
+  const int64_t items = static_cast<int64_t>(n_tiles) * runs;
   const bool in_place = p.y == p.y_in;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int4 tile = w.tiles[item / runs];
@@ -691,7 +702,7 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const __gri
       if (wm * 16 >= count) continue;
       const uint32_t at = ring + (block - first) % stages * stage_bytes;
       float acc[4][4] = {};
-      for (int ks = 0; ks < units / 2; ++ks) {
+      auto step = [&](int ks) __attribute__((always_inline)) {
         uint32_t q[2][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -707,6 +718,12 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const __gri
             mma16816<E>(acc[2 * j + 1], a[0], a[1], a[2], a[3], q[j][2], q[j][3]);
           }
         }
+      };
+      if (units == 2 * KS) {                               // the pool's whole rank: a loop without tests
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) step(ks);
+      } else {
+        for (int ks = 0; ks < units / 2; ++ks) step(ks);
       }
       const float4* slots = reinterpret_cast<const float4*>(smem + (at - s_base));
 #pragma unroll
@@ -737,9 +754,14 @@ int launch_shrink(const LoraArgs& p, const Work& w, int64_t tiles, int sms, cuda
   auto kern = lora_shrink_kernel<E, NB>;
   static std::atomic<uint64_t> done{0};
   if (set_smem_once(kern, smem, done) != WUSH_OK) return WUSH_ERR_CUDA;
-  // Split d_in until every SM has a few CTAs, but not below 256 columns a CTA.
-  unsigned splits = 1;
-  while (splits < 8 && (p.tokens + kTile - 1) / kTile * splits < 4 * sms && p.d_in / (2 * splits) >= 256) splits *= 2;
+  // Split d_in so that the tiles' clusters fill the SMs once, but not below 256 columns a
+  // CTA (the number of tiles is known on the device only: the runs' ends are taken as half
+  // a tile each).
+  constexpr int kFit = 227 * 1024 / (smem + 1024), kCtas = NB > 8 ? 1 : kFit < 3 ? kFit : 3;
+  const int64_t likely = (p.tokens + kTile - 1) / kTile + (p.n_adapters < p.tokens ? p.n_adapters : p.tokens) / 2;
+  int64_t splits = kCtas * sms / likely;
+  if (splits > p.d_in / 256) splits = p.d_in / 256;
+  splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
   cfg.blockDim = dim3(kShrinkThreads);
@@ -747,7 +769,7 @@ int launch_shrink(const LoraArgs& p, const Work& w, int64_t tiles, int sms, cuda
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = splits;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -756,6 +778,20 @@ int launch_shrink(const LoraArgs& p, const Work& w, int64_t tiles, int sms, cuda
   cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, kern, p, w) != cudaSuccess) return WUSH_ERR_CUDA;
   return launch_status();
+}
+
+template <typename E, int KS>
+int launch_expand(const LoraArgs& p, const Work& w, int64_t tiles, int sms, cudaStream_t st) {
+  // three stages of the ring where two CTAs an SM hold them, else two
+  const int row_bytes = w.row_elems * 2 + 16, terms = Split<E>::kTerms * kTile * row_bytes;
+  const int stage = kTile * kCols * 4 + kCols * row_bytes;
+  const int stages = terms + 3 * stage <= 111 * 1024 ? 3 : 2, smem = terms + stages * stage;
+  auto kern = lora_expand_kernel<E, KS>;
+  static std::atomic<uint64_t> done{0};
+  if (set_smem_once(kern, kMaxSmem, done) != WUSH_OK) return WUSH_ERR_CUDA;
+  const int fit = 227 * 1024 / (smem + 1024), ctas = fit < 1 ? 1 : fit < 3 ? fit : 3;
+  const int64_t blocks = (p.d_out + kCols - 1) / kCols, slots = int64_t(sms) * ctas, items = tiles * ((blocks + 1) / 2);
+  return launch_pdl(kern, static_cast<unsigned>(items < slots ? items : slots), kExpandThreads, smem, st, p, w, stages, 16);
 }
 
 template <typename E>
@@ -779,20 +815,13 @@ int launch_many(const LoraArgs& p, const Work& w, cudaStream_t st) {
        : p.rank <= 128 ? launch_shrink<E, 16>(p, w, tiles, sms, st)
                        : launch_shrink<E, 32>(p, w, tiles, sms, st);
   if (rc != WUSH_OK) return rc;
-  // three stages of the ring where two CTAs an SM hold them, else two
-  const int row_bytes = w.row_elems * 2 + 16, terms = Split<E>::kTerms * kTile * row_bytes;
-  const int stage = kTile * kCols * 4 + kCols * row_bytes;
-  const int stages = terms + 3 * stage <= 112 * 1024 ? 3 : 2, smem = terms + stages * stage;
-  static std::atomic<uint64_t> done{0};
-  if (set_smem_once(lora_expand_kernel<E>, kMaxSmem, done) != WUSH_OK) return WUSH_ERR_CUDA;
-  const int ctas = 224 * 1024 / (smem + 1024) < 4 ? 224 * 1024 / (smem + 1024) : 4;
-  // a run of column blocks as long as still gives every CTA a few
-  const int64_t blocks = (p.d_out + kCols - 1) / kCols, slots = int64_t(sms) * (ctas > 0 ? ctas : 1);
-  int64_t run = (p.tokens + kTile - 1) / kTile * blocks / (4 * slots);
-  run = run < 1 ? 1 : run > 16 ? 16 : run;
-  const int64_t items = tiles * ((blocks + run - 1) / run);
-  return launch_pdl(lora_expand_kernel<E>, static_cast<unsigned>(items < slots ? items : slots), kExpandThreads, smem, st,
-                    p, w, row_bytes, stages, static_cast<int>(run));
+  switch (w.row_elems) {
+    case 16: return launch_expand<E, 1>(p, w, tiles, sms, st);
+    case 32: return launch_expand<E, 2>(p, w, tiles, sms, st);
+    case 48: return launch_expand<E, 3>(p, w, tiles, sms, st);
+    case 64: return launch_expand<E, 4>(p, w, tiles, sms, st);
+    default: return launch_expand<E, 8>(p, w, tiles, sms, st);
+  }
 }
 
 // Few tokens (or a pool too large to count in shared memory) go through the cluster
