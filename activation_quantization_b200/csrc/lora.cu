@@ -19,10 +19,33 @@
 #include "sm100.cuh"
 
 namespace wush {
+
+static __device__ int g_lora_error = 0;
+
+int read_and_clear_lora_error(int* word) {
+  cudaError_t e = cudaMemcpyFromSymbol(word, g_lora_error, sizeof(int));
+  if (e != cudaSuccess) return e;
+  if (*word) {
+    const int zero = 0;
+    e = cudaMemcpyToSymbol(g_lora_error, &zero, sizeof(int));
+  }
+  return e;
+}
+
 namespace {
 
+constexpr int64_t kDefaultPolls = int64_t(1) << 40;        // waits end on the timer
+constexpr uint64_t kDeadlineNs = 4000000000ull;
+
+// A wait gave up: mark it, and let what is in flight land before the CTA's memory goes.
+__device__ __forceinline__ void report_timeout() {
+  atomicOr(&g_lora_error, kErrTimeoutBarrier);
+  const uint64_t until = sm100::globaltimer_ns() + 200000ull;
+  while (sm100::globaltimer_ns() < until) __nanosleep(1000);
+}
+
 constexpr int kMaxRank = 256;
-constexpr int64_t kMaxAdapters = 1 << 20, kMaxWidth = 1 << 24, kMaxTokens = 1 << 26;
+constexpr int64_t kMaxAdapters = 1 << 20, kMaxWidth = 1 << 24, kMaxTokens = 1 << 24;
 
 struct LoraArgs {
   const void* x;
@@ -298,12 +321,17 @@ int launch_few(const LoraArgs& p, cudaStream_t st) {
 // What bounds them: the traffic of x in shrink, of y_in and y in expand.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 64, kCols = 64;
-constexpr int kMaxSmem = 227 * 1024;
+constexpr int kMaxSmem = 226 * 1024;                      // dynamic; the rest for a kernel's own
 constexpr int kPlanThreads = 1024, kPlanAdapters = 12288;  // adapters whose counts fit the plan's shared memory
-constexpr int kShrinkThreads = 256, kExpandThreads = 256;
+constexpr int kShrinkThreads = 192;
+
+struct Counts {
+  int tiles;
+  unsigned next;                                           // pieces that expand's CTAs have drawn
+};
 
 struct Work {                                              // in the caller's workspace
-  int* n_tiles;
+  Counts* counts;
   int4* tiles;                                             // adapter, first slot, tokens, rank (0: y_in passes through)
   int* token;                                              // token of each slot (tokens sorted by adapter)
   float* up;                                               // per slot: what undoes the scaling of its terms (fp16)
@@ -324,7 +352,7 @@ size_t work_layout(int64_t tokens, int64_t n, int64_t rank, char* base, Work* w)
   };
   const int64_t row = (rank + 15) / 16 * 16;
   Work o;
-  o.n_tiles = reinterpret_cast<int*>(take(16));
+  o.counts = reinterpret_cast<Counts*>(take(sizeof(Counts)));
   o.tiles = reinterpret_cast<int4*>(take(sizeof(int4) * max_tiles(tokens, n)));
   o.token = reinterpret_cast<int*>(take(4 * tokens));
   o.up = reinterpret_cast<float*>(take(4 * tokens));
@@ -334,100 +362,139 @@ size_t work_layout(int64_t tokens, int64_t n, int64_t rank, char* base, Work* w)
   return at;
 }
 
-// Exclusive prefix sum over the CTA's threads; *total gets the sum.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
+// Exclusive prefix sums over the CTA's threads of two packed counters, *total the sums:
+// tokens in the upper half, tiles in the lower.
+__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* warp_sums, uint64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  uint64_t x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int t = warp_sums[lane];
+  uint64_t before = 0, t = warp_sums[lane];                // (every warp scans the warps' sums)
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, t, o);
-      if (lane >= o) t += y;
-    }
-    warp_sums[lane] = t;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(0xffffffffu, t, o);
+    if (lane >= o) t += y;
   }
+  *total = __shfl_sync(0xffffffffu, t, 31);
+  before = __shfl_sync(0xffffffffu, t, warp ? warp - 1 : 0);
   __syncthreads();
-  const int before = warp ? warp_sums[warp - 1] : 0;
-  *total = warp_sums[31];
-  __syncthreads();
-  return before + x - v;
+  return (warp ? before : 0) + x - v;
 }
 
-// One CTA.  Shared memory: a counter for each adapter and one for the tokens without.
-// (The order of an adapter's tokens is left to the atomics.  A token's result is the same
-// in every place of a tile: rows of an MMA do not meet, and everything else is per row.)
+// One CTA.  ORDERED: an adapter's tokens keep their order, so that the rows of a request lie
+// side by side in a tile and shrink can fetch them in blocks: every warp has a stretch of the
+// tokens and counters of its own, in shared memory [32][n + 1].  Otherwise (pools of more
+// than kOrderedAdapters) there is one set of counters, and the order is left to the atomics;
+// a token's result is the same in every place of a tile, since rows of an MMA do not meet and
+// everything else is per row.
+constexpr int kOrderedAdapters = 1024;
+
+template <bool ORDERED>
 __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const int32_t* __restrict__ adapter, int64_t tokens,
                                                                  int n, int rank, const int32_t* __restrict__ ranks,
                                                                  Work w) {
-  extern __shared__ int count[];                           // [n + 1], then the next free slot of each
-  __shared__ int warp_sums[32];
-  const int tid = threadIdx.x, lane = tid & 31;
-  for (int i = tid; i <= n; i += kPlanThreads) count[i] = 0;
+  extern __shared__ int count[];                           // counts, then the next free slot of each
+  __shared__ uint64_t warp_sums[32];
+  constexpr int kSets = ORDERED ? 32 : 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int* mine = count + (ORDERED ? warp * (n + 1) : 0);
+  for (int i = tid; i < kSets * (n + 1); i += kPlanThreads) count[i] = 0;
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
   __syncthreads();
-  // the adapters of eight tokens of each thread at a time, all asked for before any is used
-  int mine8[8];
+  // a warp's stretch, 256 tokens at a time, all asked for before any is used
+  const int64_t stretch = (tokens + kPlanThreads - 1) / kPlanThreads * 32, from = warp * stretch;
+  const int64_t to = from + stretch < tokens ? from + stretch : tokens;
+  int group[8];
   auto fetch = [&](int64_t t0) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int64_t t = t0 + j * kPlanThreads + tid;
-      const int g = t < tokens ? adapter[t] : n;
-      mine8[j] = t >= tokens ? -1 : g >= 0 && g < n ? g : n;
+      const int64_t t = t0 + j * 32 + lane;
+      const int g = t < to ? adapter[t] : 0;
+      group[j] = t >= to ? -1 : g >= 0 && g < n ? g : n;
     }
   };
-  for (int64_t t0 = 0; t0 < tokens; t0 += 8 * kPlanThreads) {
+  auto rank_of = [&](int i) {
+    const int k = ranks ? ranks[i] : rank;
+    return k < 0 ? 0 : k > rank ? rank : k;
+  };
+  const int my_rank = tid < n ? rank_of(tid) : 0;
+  for (int64_t t0 = from; t0 < to; t0 += 256) {
     fetch(t0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (t0 + j * kPlanThreads >= tokens) break;
-      const int g = mine8[j];
+      if (t0 + j * 32 >= to) break;                        // (the whole warp alike)
+      const int g = group[j];
       const uint32_t same = __match_any_sync(0xffffffffu, g);
-      if (g >= 0 && lane == __ffs(same) - 1) atomicAdd(&count[g], __popc(same));
-    }
-  }
-  __syncthreads();
-  int slots = 0, tiles = 0;
-  for (int i0 = 0; i0 <= n; i0 += kPlanThreads) {
-    const int i = i0 + tid, c = i <= n ? count[i] : 0, cut = (c + kTile - 1) / kTile;
-    int all_c, all_t;
-    const int first = slots + block_scan(c, warp_sums, &all_c);
-    const int tile = tiles + block_scan(cut, warp_sums, &all_t);
-    if (c) {
-      int k = 0;
-      if (i < n) {
-        k = ranks ? ranks[i] : rank;
-        k = k < 0 ? 0 : k > rank ? rank : k;
+      if (g >= 0 && lane == __ffs(same) - 1) {
+        if (ORDERED) mine[g] += __popc(same);
+        else atomicAdd(&mine[g], __popc(same));
       }
-      for (int j = 0; j < cut; ++j)
-        w.tiles[tile + j] = make_int4(i, first + j * kTile, c - j * kTile < kTile ? c - j * kTile : kTile, k);
+      __syncwarp();
     }
-    if (i <= n) count[i] = first;
-    slots += all_c;
-    tiles += all_t;
   }
-  if (tid == 0) *w.n_tiles = tiles;
   __syncthreads();
-  for (int64_t t0 = 0; t0 < tokens; t0 += 8 * kPlanThreads) {
-    if (tokens > 8 * kPlanThreads) fetch(t0);
+  uint64_t base = 0;
+  for (int i0 = 0; i0 <= n; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    int c = 0;
+    if (i <= n)
+      for (int q = 0; q < kSets; ++q) c += count[q * (n + 1) + i];
+    const int k = i >= n ? 0 : i0 == 0 ? my_rank : rank_of(i), tiles = (c + kTile - 1) / kTile;
+    uint64_t all;
+    const uint64_t at = base + block_scan(uint64_t(c) << 32 | uint64_t(tiles), warp_sums, &all);
+    const int first = static_cast<int>(at >> 32), tile = static_cast<int>(at);
+    base += all;
+    // an adapter's tiles: its thread writes a few, its warp many
+    auto cut = [&](int to_tile, int g, int slot, int tokens_g, int rank_g, int j) {
+      const int left = tokens_g - j * kTile;
+      w.tiles[to_tile + j] = make_int4(g, slot + j * kTile, left < kTile ? left : kTile, rank_g);
+    };
+    if (tiles <= 16)
+      for (int j = 0; j < tiles; ++j) cut(tile, i, first, c, k, j);
+    for (uint32_t many = __ballot_sync(0xffffffffu, tiles > 16); many; many &= many - 1) {
+      const int of = __ffs(many) - 1;
+      const int c2 = __shfl_sync(0xffffffffu, c, of), k2 = __shfl_sync(0xffffffffu, k, of);
+      const int f2 = __shfl_sync(0xffffffffu, first, of), i2 = __shfl_sync(0xffffffffu, i, of);
+      const int t2 = __shfl_sync(0xffffffffu, tile, of), nt = __shfl_sync(0xffffffffu, tiles, of);
+      for (int j = lane; j < nt; j += 32) cut(t2, i2, f2, c2, k2, j);
+    }
+    if (c) {
+      int slot = first;
+      for (int q = 0; q < kSets; ++q) {
+        const int here = count[q * (n + 1) + i];
+        count[q * (n + 1) + i] = slot;
+        slot += here;
+      }
+    }
+  }
+  if (tid == 0) *w.counts = Counts{static_cast<int>(base), 0u};
+  __syncthreads();
+  for (int64_t t0 = from; t0 < to; t0 += 256) {
+    if (stretch > 256) fetch(t0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (t0 + j * kPlanThreads >= tokens) break;
-      const int g = mine8[j];
+      if (t0 + j * 32 >= to) break;
+      const int g = group[j];
       const uint32_t same = __match_any_sync(0xffffffffu, g);
       const int leader = __ffs(same) - 1;
       int at = 0;
-      if (g >= 0 && lane == leader) at = atomicAdd(&count[g], __popc(same));
+      if (g >= 0 && lane == leader) {
+        if (ORDERED) {
+          at = mine[g];
+          mine[g] = at + __popc(same);
+        } else {
+          at = atomicAdd(&mine[g], __popc(same));
+        }
+      }
       at = __shfl_sync(0xffffffffu, at, leader);
-      if (g >= 0) w.token[at + __popc(same & ((1u << lane) - 1))] = static_cast<int>(t0 + j * kPlanThreads + tid);
+      if (g >= 0) w.token[at + __popc(same & ((1u << lane) - 1))] = static_cast<int>(t0 + j * 32 + lane);
+      __syncwarp();
     }
   }
 }
@@ -435,164 +502,250 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const int32_t* 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {   // the rest of the 16 is zeroed
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+// Four rows of a matrix whose tensor map has boxes one row high, side by side in shared
+// memory; rows beyond the matrix read as zero.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int col, int4 rows, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w),
+      "r"(sm100::smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, int col, int row, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(row), "r"(sm100::smem_u32(bar))
+      : "memory");
+}
+
+// A wait that gives up sets the CTA's flag, and every later wait then gives up at once: the
+// roles run on to the CTA's common barriers, and the error is reported at the end.
+__device__ __forceinline__ void wait_or_flag(uint64_t* bar, uint32_t parity, int* abort_flag) {
+  if (!sm100::mbar_wait_bounded(bar, parity, kDefaultPolls, kDeadlineNs, abort_flag))
+    *static_cast<volatile int*>(abort_flag) = 1;
+}
+
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+// ---- tcgen05, 64 rows a tile (one 16-row slice in each quarter of TMEM's lanes)
+template <typename E>
+__host__ __device__ constexpr uint32_t idesc_f16_m64(uint32_t n) {        // K-major A and B of E, fp32 D
+  const uint32_t type = std::is_same<E, __half>::value ? 0u : 1u;
+  return (1u << 4) | (type << 7) | (type << 10) | ((n >> 3) << 17) | ((64u >> 4) << 24);
+}
+__device__ __forceinline__ void tc_mma(uint32_t tmem_d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(sm100::desc_kmajor_sw128(a)), "l"(sm100::desc_kmajor_sw128(b)), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 16 lanes x 8 columns: the warp's slice of a 64-row D, held like an m16n8 accumulator
+// (lane: row lane / 4 and + 8, columns 2 (lane % 4) and + 1).
+__device__ __forceinline__ void tmem_ld_16x8(uint32_t addr, float (&v)[4]) {
+  uint32_t r[4];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-constexpr int kBk = 64;
+constexpr int kBk = 128;                                  // columns of d_in a stage: two operand tiles of 64
 
-// NB: blocks of 8 ranks.  A stage holds 64 columns of the tile's x and of A, rows of 128
-// bytes whose 16-byte units are permuted by the row (unit ^ row % 8), so that the MMA
-// fragments load without bank conflicts.  Behind the stages: the CTA's s, fp32
-// [kTile][kRow], into which the MMA accumulators are added every 1024 columns.  Of a
-// stage's four MMA steps the first four warps (16 tokens each) take two and the last four
-// the others, so no chain of MMAs is longer than 32 steps.
-template <int NB>
-__host__ __device__ constexpr int shrink_stages() { return NB <= 4 ? 4 : 3; }
-template <int NB>
-constexpr int shrink_smem() {
-  return shrink_stages<NB>() * (kTile + NB * 8) * 128 + kTile * (NB * 8 + 4) * 4;
-}
+// One warp asks for the tiles of x (rows gathered by TMA) and of A, one issues the MMAs, four
+// take D out of TMEM.  A stage holds 128 columns as two halves of 64, rows of 128 bytes with
+// the 128-byte swizzle.  D is added to fp32 registers and begun anew every kChain stages: the
+// tensor core's own additions cut off low bits, and 32 of them in a row stay near fp32's
+// rounding of the sums (4096 tokens x 12288, rank 128: a chain over a CTA's whole d_in gave
+// 2.8e-6 relative to the result, chains of 32 give 1.0e-6).
+//
+// (Copies by cp.async would have to pass a proxy fence before the MMAs may read them, and
+// that fence waits for the copies still in flight too: 30 us at 4096 tokens x 12288, rank 64.)
+constexpr int kChain = 4;
 
-template <typename E, int NB>
-__global__ void __launch_bounds__(kShrinkThreads, NB <= 8 ? 3 : 1) lora_shrink_kernel(const __grid_constant__ LoraArgs p,
-                                                                     const __grid_constant__ Work w) {
-  constexpr int kR = NB * 8, kRow = kR + 4, kT = Split<E>::kTerms, kStage = (kTile + kR) * 128;
-  constexpr int kShrinkStages = shrink_stages<NB>();
-  extern __shared__ __align__(128) unsigned char smem[];
-  float* sum = reinterpret_cast<float*>(smem + kShrinkStages * kStage);
+template <int R>
+struct Shrink {
+  static constexpr int kHalf = (kTile + R) * 128, kStage = 2 * kHalf;
+  static constexpr int kStages = R <= 128 ? 3 : 2;
+  static constexpr int kAcc = R <= 128 ? 2 : 1;            // D's that chains take in turn
+  static constexpr int kTmem = kAcc * R < 32 ? 32 : kAcc * R;
+  static constexpr int kRow = R + 4;                       // floats of a row of the CTA's s, laid over the stages
+  static constexpr int kSmem = kStages * kStage + 1024;    // (the swizzle's 8-row groups are 1024-byte aligned)
+  static constexpr int kCtas = 227 * 1024 / (kSmem + 1536);   // an SM
+  static_assert(kTile * kRow * 4 <= kStages * kStage, "s fits over the stages");
+  // CTAs of a cluster wait for one another, so none may hold an SM's place while it waits for
+  // TMEM that a CTA in the same state holds.  A kernel's share of TMEM is no larger than its
+  // share of shared memory: whatever CTAs an SM holds, their TMEM is there.
+  static_assert(kTmem * 227 <= 512 * (kSmem / 1024), "TMEM goes by shared memory");
+};
+
+template <typename E, int R>
+__global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __grid_constant__ LoraArgs p,
+                                                                     const __grid_constant__ Work w,
+                                                                     const __grid_constant__ CUtensorMap map_x,
+                                                                     const __grid_constant__ CUtensorMap map_x8,
+                                                                     const __grid_constant__ CUtensorMap map_a) {
+  using L = Shrink<R>;
+  constexpr int kT = Split<E>::kTerms;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t full[L::kStages], empty[L::kStages], d_full[L::kAcc], d_empty[L::kAcc];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  const uint32_t base = (sm100::smem_u32(smem_raw) + 1023u) & ~1023u;
+  float* sum = reinterpret_cast<float*>(smem_raw + (base - sm100::smem_u32(smem_raw)));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t splits;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(splits));
   const uint32_t cta = sm100::cluster_ctarank();
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < L::kStages; ++i) {
+      sm100::mbar_init(&full[i], 1);
+      sm100::mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < L::kAcc; ++i) {
+      sm100::mbar_init(&d_full[i], 1);
+      sm100::mbar_init(&d_empty[i], 4);
+    }
+    sm100::fence_barrier_init();
+    sm100::prefetch_tmap(&map_x);
+    sm100::prefetch_tmap(&map_x8);
+    sm100::prefetch_tmap(&map_a);
+  }
+  __syncwarp();
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
   const int item = blockIdx.x / splits;
-  if (item >= *w.n_tiles) return;
+  if (item >= w.counts->tiles) return;
   const int4 tile = w.tiles[item];
   const int k = tile.w, count = tile.z;
   if (k == 0) return;                                      // (all CTAs of a cluster decide alike)
-  const E* A = static_cast<const E*>(p.a) + static_cast<int64_t>(tile.x) * p.rank * p.d_in;
+  if (warp == 0) sm100::tmem_alloc(&tmem_slot, L::kTmem);
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
   // this CTA's columns
   const int steps = (p.d_in + kBk - 1) / kBk, per = (steps + splits - 1) / splits;
-  const int first = cta * per < steps ? cta * per : steps, last = first + per < steps ? first + per : steps;
-
-  const uint32_t base = sm100::smem_u32(smem);
-  const int unit = tid & 7, row0 = tid >> 3;               // this thread copies unit ``unit`` of rows row0 + 32 j
-  const E* x[2];
+  const int first = cta * per < steps ? cta * per : steps, n = (first + per < steps ? first + per : steps) - first;
+  const uint32_t ranks16 = (k + 15) / 16 * 16;             // columns of D that the MMAs compute
+  float total[R / 8][4] = {};
+  if (warp == 4) {
+    // lane: half of the stage, eight rows of x: one block where they follow one another (TMA
+    // takes rows so four times as fast as gathered ones), else two gathers (rows without a token
+    // lie beyond x and read as zero; groups without one are left as they are)
+    const int half = (lane >> 3) & 1, row = (lane & 7) * 8, none = static_cast<int>(p.tokens);
+    const int groups = (count + 7) / 8;
+    const bool mine = lane < 16 && row < count;
+    int rows[8];
+    bool block = row + 8 <= count;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int r = row0 + 32 * j;
-    x[j] = r < count ? static_cast<const E*>(p.x) + w.token[tile.y + r] * p.x_stride : nullptr;
-  }
-  auto load = [&](int step) {
-    const int col = step * kBk + unit * 8;
-    const bool in = col < p.d_in;                          // (d_in is a multiple of 32)
-    const uint32_t to = base + (step - first) % kShrinkStages * kStage + ((unit ^ (row0 & 7)) << 4);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      cp_async16(to + (row0 + 32 * j) * 128, x[j] && in ? x[j] + col : static_cast<const E*>(p.x), x[j] && in ? 16 : 0);
-#pragma unroll
-    for (int j = 0; j < (NB + 3) / 4; ++j) {
-      const int r = row0 + 32 * j;
-      if (r >= kR) break;
-      const bool ok = in && r < k;
-      cp_async16(to + (kTile + r) * 128, ok ? A + static_cast<int64_t>(r) * p.d_in + col : A, ok ? 16 : 0);
+    for (int j = 0; j < 8; ++j) {
+      rows[j] = mine && row + j < count ? w.token[tile.y + row + j] : none;
+      block = block && rows[j] == rows[0] + j;
     }
-  };
-  float acc[NB][4] = {};
-  const int wm = warp & 3, wk = warp >> 2;                 // 16 tokens; half of a stage's steps
-  const bool active = wm * 16 < count;
-  const int frow = wm * 16 + (lane >> 2), fcol = (lane & 3) * 2;
-  auto flush = [&](bool fresh) {
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      float2* lo = reinterpret_cast<float2*>(sum + frow * kRow + b * 8 + fcol);
-      float2* hi = reinterpret_cast<float2*>(sum + (frow + 8) * kRow + b * 8 + fcol);
-      if (fresh) {
-        *lo = make_float2(acc[b][0], acc[b][1]);
-        *hi = make_float2(acc[b][2], acc[b][3]);
-      } else {
-        const float2 u = *lo, v = *hi;
-        *lo = make_float2(u.x + acc[b][0], u.y + acc[b][1]);
-        *hi = make_float2(v.x + acc[b][2], v.y + acc[b][3]);
+    for (int i = 0; i < n; ++i) {
+      const int s = i % L::kStages, col = (first + i) * kBk;
+      wait_or_flag(&empty[s], ((i / L::kStages) & 1) ^ 1, &abort_flag);
+      const uint32_t to = base + s * L::kStage;
+      if (lane == 0) {
+        sm100::mbar_arrive_expect_tx(&full[s], 2 * (R + groups * 8) * 128);
+        tma_tile(to + kTile * 128, &map_a, col, tile.x * p.rank, &full[s]);
+        tma_tile(to + L::kHalf + kTile * 128, &map_a, col + 64, tile.x * p.rank, &full[s]);
       }
-      acc[b][0] = acc[b][1] = acc[b][2] = acc[b][3] = 0.0f;
+      __syncwarp();
+      const uint32_t dst = to + half * L::kHalf + row * 128;
+      if (mine && block) {
+        tma_tile(dst, &map_x8, col + half * 64, rows[0], &full[s]);
+      } else if (mine) {
+        tma_gather4(dst, &map_x, col + half * 64, make_int4(rows[0], rows[1], rows[2], rows[3]), &full[s]);
+        tma_gather4(dst + 512, &map_x, col + half * 64, make_int4(rows[4], rows[5], rows[6], rows[7]), &full[s]);
+      }
     }
-  };
-  // the first set of warps stores or adds its accumulators, then the second adds its own
-  auto flush_all = [&](bool fresh) {
-    if (active && wk == 0) flush(fresh);
-    __syncthreads();
-    if (active && wk == 1) flush(false);
-    __syncthreads();
-  };
-  bool fresh = true;
+  } else if (warp == 5) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_f16_m64<E>(ranks16);
+      for (int i = 0; i < n; ++i) {
+        const int s = i % L::kStages, chain = i / kChain, d = chain % L::kAcc;
+        if (i % kChain == 0) wait_or_flag(&d_empty[d], ((chain / L::kAcc) & 1) ^ 1, &abort_flag);
+        wait_or_flag(&full[s], (i / L::kStages) & 1, &abort_flag);
+        sm100::tc_fence_after();
+        const uint32_t at = base + s * L::kStage;
 #pragma unroll
-  for (int s = 0; s < kShrinkStages - 1; ++s) {
-    if (first + s < last) load(first + s);
-    cp_async_commit();
-  }
-  for (int step = first; step < last; ++step) {
-    cp_async_wait<kShrinkStages - 2>();
-    __syncthreads();
-    if (step + kShrinkStages - 1 < last) load(step + kShrinkStages - 1);
-    cp_async_commit();
-    if (active) {
-      const uint32_t at = base + (step - first) % kShrinkStages * kStage;
-      // FULL: every block of 8 ranks is in use, so that the loads need not wait for tests
-      auto multiply = [&](auto full) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < kBk / 32; ++i) {
-          const int ks = wk * (kBk / 32) + i;
-          uint32_t a[4];
-          const int ar = wm * 16 + (lane & 15);
-          ldmatrix4(at + ar * 128 + (((2 * ks + (lane >> 4)) ^ (ar & 7)) << 4), a);
-#pragma unroll
-          for (int b = 0; b < NB; b += 2) {
-            if (!full.value && b * 8 >= k) break;
-            uint32_t q[4];
-            const int br = b * 8 + (lane & 7) + ((lane >> 4) << 3);
-            ldmatrix4(at + (kTile + br) * 128 + (((2 * ks + ((lane >> 3) & 1)) ^ (br & 7)) << 4), q);
-            mma16816<E>(acc[b], a[0], a[1], a[2], a[3], q[0], q[1]);
-            mma16816<E>(acc[b + 1], a[0], a[1], a[2], a[3], q[2], q[3]);
-          }
+        for (int ks = 0; ks < kBk / 16; ++ks) {
+          const uint32_t a = at + (ks >> 2) * L::kHalf + (ks & 3) * 32;
+          tc_mma(tmem + d * R, a, a + kTile * 128, idesc, i % kChain != 0 || ks > 0);
         }
-      };
-      if (k > (NB - 2) * 8) multiply(std::true_type{});
-      else multiply(std::false_type{});
+        sm100::tc_commit(&empty[s]);
+        if (i % kChain == kChain - 1 || i == n - 1) sm100::tc_commit(&d_full[d]);
+      }
     }
-    if ((step - first) % 16 == 15) {
-      flush_all(fresh);
-      fresh = false;
+    __syncwarp();
+  } else if (warp < 4) {
+    for (int chain = 0; chain * kChain < n; ++chain) {
+      const int d = chain % L::kAcc;
+      wait_or_flag(&d_full[d], (chain / L::kAcc) & 1, &abort_flag);
+      sm100::tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < R / 8; b += 4) {                 // (four loads in flight)
+        float v[4][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (b + q < R / 8)
+            tmem_ld_16x8(tmem + (static_cast<uint32_t>(warp * 32) << 16) + d * R + (b + q) * 8, v[q]);
+        sm100::tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (b + q < R / 8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) total[b + q][e] += v[q][e];
+          }
+      }
+      sm100::tc_fence_before();
+      if (lane == 0) sm100::mbar_arrive(&d_empty[d]);
     }
   }
-  flush_all(fresh);
+  __syncthreads();                                         // the stages have been read: s goes over them
+  if (warp < 4) {
+#pragma unroll
+    for (int b = 0; b < R / 8; ++b) {                      // (columns from ranks16 on are never read)
+      float* o = sum + (warp * 16 + (lane >> 2)) * L::kRow + b * 8 + (lane & 3) * 2;
+      *reinterpret_cast<float2*>(o) = make_float2(total[b][0], total[b][1]);
+      *reinterpret_cast<float2*>(o + 8 * L::kRow) = make_float2(total[b][2], total[b][3]);
+    }
+  }
+  sm100::tc_fence_before();
   sm100::cluster_sync();
+  if (warp == 0) {
+    sm100::tc_fence_after();
+    sm100::tmem_dealloc(tmem, L::kTmem);
+  }
 
   // The cluster's CTAs share the tile's rows; a warp sums the parts of a row in their
-  // order, scales, and stores the terms.
+  // order, scales, and stores the terms.  (Ranks from k on are padding: A may hold anything
+  // there.)
   const float sc = p.scale ? p.scale[tile.x] : 1.0f;
   const uint32_t sum_at = sm100::smem_u32(sum);
   E* terms = static_cast<E*>(w.terms);
-  const int kp = (k + 15) / 16 * 16;
   for (int r = cta + splits * warp; r < count; r += splits * (kShrinkThreads / 32)) {
-    float v[(kR + 31) / 32];
+    float v[(R + 31) / 32];
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < (kR + 31) / 32; ++i) {
+    for (int i = 0; i < (R + 31) / 32; ++i) {
       const int c = i * 32 + lane;
       v[i] = 0.0f;
-      if (c < kp) {
-        for (uint32_t q = 0; q < splits; ++q) v[i] += ld_cluster(sm100::mapa_shared(sum_at + (r * kRow + c) * 4, q));
+      if (c < k) {
+        float part[8];
+#pragma unroll
+        for (uint32_t q = 0; q < 8; ++q)
+          part[q] = q < splits ? ld_cluster(sm100::mapa_shared(sum_at + (r * L::kRow + c) * 4, q)) : 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[i] += part[q];
         v[i] *= sc;
       }
       top = fmaxf(top, fabsf(v[i]));
@@ -605,9 +758,9 @@ __global__ void __launch_bounds__(kShrinkThreads, NB <= 8 ? 3 : 1) lora_shrink_k
       if (lane == 0) w.up[tile.y + r] = up;
     }
 #pragma unroll
-    for (int i = 0; i < (kR + 31) / 32; ++i) {
+    for (int i = 0; i < (R + 31) / 32; ++i) {
       const int c = i * 32 + lane;
-      if (c >= kp) continue;
+      if (c >= static_cast<int>(ranks16)) continue;
       E t[kT];
       split<E>(v[i] * down, t);
 #pragma unroll
@@ -616,152 +769,326 @@ __global__ void __launch_bounds__(kShrinkThreads, NB <= 8 ? 3 : 1) lora_shrink_k
     }
   }
   sm100::cluster_sync();                                   // no CTA leaves while another may read its sums
+  if (tid == 0 && *static_cast<volatile int*>(&abort_flag)) report_timeout();
 }
 
-// A CTA takes a tile and a run of blocks of 64 columns.  The tile's terms stay in shared
-// memory; B and y_in come through a ring, ahead of the products.  A warp has 16 tokens x 32
-// columns.  Column order: of 16 columns, MMA block 0 takes those with bit 1 clear and block
-// 1 the others (the rows of B are put into shared memory in that order), so that a thread's
-// values of both blocks are four consecutive columns: one 16-byte access of y each.  y_in
-// goes into slots that only the thread itself reads.  Rows of B and of the terms are 16
-// bytes longer than the ranks, which spreads a fragment's rows over the banks.
-// KS: the rank's MMA steps that have an unrolled loop.
-template <typename E, int KS>
+// A CTA goes along a tile in blocks of 64 columns: D = B s is one 64 x 64 product in TMEM.
+//
+// The terms lie side by side in k, term t of rank j at k = t * row_elems + j, in operand tiles
+// of 64 (128-byte rows, 128-byte swizzle); each term's steps meet the same rows of B.  D comes
+// back in the layout of an m16n8 accumulator; of 16 columns, its block 0 is given those with
+// bit 1 clear and block 1 the others (TMA gathers B's rows in that order), so that a thread's
+// values of both blocks are four consecutive columns: one 16-byte access of y each.
+//
+// One warp asks for the terms and B, one issues the MMAs, eight add D to y_in and store.  These
+// fetch their own y_in, by asynchronous copies into slots that only the thread itself reads, so
+// the roles meet on barriers in shared memory alone.
+constexpr int kExpandThreads = 352;
+constexpr int kAddThreads = 256;
+
+struct Expand {
+  int b_bytes, terms_bytes, b_slots, y_slots, smem;
+};
+
+template <typename E>
+Expand expand_layout(int row_elems) {
+  Expand l;
+  l.terms_bytes = (Split<E>::kTerms * row_elems + 63) / 64 * kTile * 128;
+  l.b_bytes = (row_elems + 63) / 64 * kCols * 128;
+  // two CTAs an SM where they fit, with up to four slots of y_in and of B; else one
+  const int y = kTile * kCols * 4, half = 111 * 1024, room = l.terms_bytes + 2 * (y + l.b_bytes) <= half ? half : kMaxSmem - 1024;
+  l.b_slots = l.y_slots = 2;
+  int left = room - l.terms_bytes - 2 * (y + l.b_bytes);
+  for (int i = 0; i < 2; ++i) {
+    if (left >= l.b_bytes) ++l.b_slots, left -= l.b_bytes;
+    if (left >= y) ++l.y_slots, left -= y;
+  }
+  l.smem = l.terms_bytes + l.b_slots * l.b_bytes + l.y_slots * y + 1024;
+  return l;
+}
+
+template <typename E>
 __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const __grid_constant__ LoraArgs p,
-                                                                     const __grid_constant__ Work w, int stages,
-                                                                     int most_run) {
-  constexpr int kT = Split<E>::kTerms;
-  const int row_bytes = w.row_elems * 2 + 16;
-  extern __shared__ __align__(128) unsigned char smem[];   // terms [kT][kTile] rows; per stage: y_in slots, B rows
+                                                                     const __grid_constant__ Work w,
+                                                                     const __grid_constant__ Expand l,
+                                                                     const __grid_constant__ CUtensorMap map_s,
+                                                                     const __grid_constant__ CUtensorMap map_b) {
+  constexpr int kT = Split<E>::kTerms, kSlot = kTile * kCols * 4;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t b_full[4], b_empty[4], d_full[2], d_empty[2], s_full, s_empty, piece_full[2],
+      piece_empty[2];
+  __shared__ unsigned piece[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  const uint32_t s_base = (sm100::smem_u32(smem_raw) + 1023u) & ~1023u, b_ring = s_base + l.terms_bytes;
+  const uint32_t y_ring = b_ring + l.b_slots * l.b_bytes;
+  unsigned char* smem = smem_raw + (s_base - sm100::smem_u32(smem_raw));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int wm = warp & 3, wn = warp >> 2, g = lane >> 2, c = lane & 3;
-  constexpr int kSlots = kTile * kCols * 4;
-  const int stage_bytes = kSlots + kCols * row_bytes;
-  const uint32_t s_base = sm100::smem_u32(smem), ring = s_base + kT * kTile * row_bytes;
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < 4; ++i) {
+      sm100::mbar_init(&b_full[i], 1);
+      sm100::mbar_init(&b_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      sm100::mbar_init(&d_full[i], 1);
+      sm100::mbar_init(&d_empty[i], kAddThreads / 32);
+      sm100::mbar_init(&piece_full[i], 1);
+      sm100::mbar_init(&piece_empty[i], kAddThreads / 32 + 2);
+    }
+    sm100::mbar_init(&s_full, 1);
+    sm100::mbar_init(&s_empty, 1);
+    sm100::fence_barrier_init();
+    sm100::prefetch_tmap(&map_s);
+    sm100::prefetch_tmap(&map_b);
+  }
+  __syncwarp();
+  if (warp == 8) sm100::tmem_alloc(&tmem_slot, 2 * kCols);
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
-  // a run of column blocks as long as still gives every CTA a few items
-  const int blocks = (p.d_out + kCols - 1) / kCols, n_tiles = *w.n_tiles;
-  int run = static_cast<int>(static_cast<int64_t>(n_tiles) * blocks / (4 * gridDim.x));
-  run = run < 2 ? 2 : run > most_run ? most_run : run;
-  const int runs = (blocks + run - 1) / run;
-  const int64_t items = static_cast<int64_t>(n_tiles) * runs;
-  const bool in_place = p.y == p.y_in;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int4 tile = w.tiles[item / runs];
-    const int first = static_cast<int>(item % runs) * run, last = first + run < blocks ? first + run : blocks;
-    const int k = tile.w, count = tile.z;
-    if (k == 0 && in_place) continue;
-    const int r0 = wm * 16 + g, r1 = r0 + 8;
-    const int64_t t0 = r0 < count ? w.token[tile.y + r0] : -1, t1 = r1 < count ? w.token[tile.y + r1] : -1;
-    const int units = (k + 15) / 16 * 2;
-    const E* B = static_cast<const E*>(p.b) + static_cast<int64_t>(tile.x) * p.d_out * p.rank;
-    const E* S = static_cast<const E*>(w.terms) + static_cast<int64_t>(tile.y) * kT * w.row_elems;
-    __syncthreads();                                       // the run before is done with shared memory
-    for (int i = tid; i < count * kT * units; i += kExpandThreads) {
-      const int r = i / units, u = i % units;              // r: slot * kT + term
-      cp_async16(s_base + (r % kT * kTile + r / kT) * row_bytes + u * 16, S + static_cast<int64_t>(r) * w.row_elems + u * 8,
-                 16);
-    }
-    auto load = [&](int block) {
-      const int n0 = block * kCols;
-      const uint32_t to = ring + (block - first) % stages * stage_bytes;
-      for (int i = tid; i < kCols * units; i += kExpandThreads) {
-        const int n = i / units, u = i % units, col = u * 8;
-        int bytes = n0 + n < p.d_out ? (k - col) * 2 : 0;  // columns from k on are padding that may hold anything
-        bytes = bytes < 0 ? 0 : bytes > 16 ? 16 : bytes;
-        const int at = (n & ~15) | ((n >> 1) & 1) << 3 | ((n >> 2) & 3) << 1 | (n & 1);
-        cp_async16(to + kSlots + at * row_bytes + u * 16, bytes ? B + static_cast<int64_t>(n0 + n) * p.rank + col : B,
-                   bytes);
+  // All tiles' column blocks lie in one row, cut into pieces that the CTAs take as they come to
+  // them: the first piece by the CTA's number, the later ones from a counter (SMs do not all get
+  // the same share of the memory's bandwidth).  The first warp draws a piece ahead of its use
+  // and passes it to the roles.
+  const int blocks = (p.d_out + kCols - 1) / kCols;
+  const int64_t all = static_cast<int64_t>(w.counts->tiles) * blocks;
+  // (A short row goes in equal pieces: a tile's terms are fetched anew for each piece.)
+  const int64_t even = (all + gridDim.x - 1) / gridDim.x;
+  const int64_t size = even < 64 ? (even > 0 ? even : 1) : even / 6 < 32 ? even / 6 : 32;
+  struct Piece {
+    int4 tile;                                             // adapter, first slot, tokens, rank
+    int first, blocks;
+  };
+  int turn = 0;
+  // Calls f for each stretch of a piece within one tile, piece after piece, until none is left.
+  auto for_pieces = [&](auto f) __attribute__((always_inline)) {
+    for (;; ++turn) {
+      wait_or_flag(&piece_full[turn & 1], (turn >> 1) & 1, &abort_flag);
+      int64_t pos = piece[turn & 1] * size;
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&piece_empty[turn & 1]);
+      if (pos >= all || *static_cast<volatile int*>(&abort_flag)) return;
+      const int64_t to = pos + size < all ? pos + size : all;
+      while (pos < to) {
+        Piece q;
+        q.tile = w.tiles[pos / blocks];
+        q.first = static_cast<int>(pos % blocks);
+        q.blocks = to - pos < blocks - q.first ? static_cast<int>(to - pos) : blocks - q.first;
+        f(q);
+        pos += q.blocks;
       }
-      if (p.y_in) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int n = n0 + wn * 32 + j * 16 + c * 4;
-          if (n >= p.d_out) continue;
-          if (t0 >= 0) cp_async16(to + ((2 * j) * kExpandThreads + tid) * 16, p.y_in + t0 * p.y_in_stride + n, 16);
-          if (t1 >= 0) cp_async16(to + ((2 * j + 1) * kExpandThreads + tid) * 16, p.y_in + t1 * p.y_in_stride + n, 16);
+    }
+  };
+
+  if (warp == 10) {
+    if (lane == 0) {
+      unsigned index = blockIdx.x;
+      for (int i = 0;; ++i) {
+        wait_or_flag(&piece_empty[i & 1], ((i >> 1) & 1) ^ 1, &abort_flag);
+        piece[i & 1] = index;
+        sm100::mbar_arrive(&piece_full[i & 1]);
+        if (index * size >= all || *static_cast<volatile int*>(&abort_flag)) break;
+        index = gridDim.x + atomicAdd(&w.counts->next, 1u);
+      }
+    }
+    __syncwarp();
+  } else
+  if (warp == 8) {
+    int nb = 0, ns = 0;                                    // blocks of B and tiles' terms asked for so far
+    for_pieces([&](const Piece& q) {
+      const int k = q.tile.w, units = (k + 63) / 64;
+      if (k == 0) return;
+      wait_or_flag(&s_empty, (ns & 1) ^ 1, &abort_flag);
+      ++ns;
+      if (lane == 0) {
+        sm100::mbar_arrive_expect_tx(&s_full, l.terms_bytes);
+        for (int i = 0; i < l.terms_bytes / (kTile * 128); ++i)
+          tma_tile(s_base + i * (kTile * 128), &map_s, i * 64, q.tile.y, &s_full);
+      }
+      // lane: rows of B in the order of D's columns, four at a time (16 groups for 64 columns)
+      const int group = lane & 15, n16 = (group >> 2) * 16 + ((group >> 1) & 1) * 2 + (group & 1) * 8;
+      for (int b = 0; b < q.blocks; ++b, ++nb) {
+        const int s = nb % l.b_slots, n0 = (q.first + b) * kCols + n16;
+        wait_or_flag(&b_empty[s], ((nb / l.b_slots) & 1) ^ 1, &abort_flag);
+        if (lane == 0) sm100::mbar_arrive_expect_tx(&b_full[s], units * kCols * 128);
+        __syncwarp();
+        // (columns beyond d_out read the next adapter's rows; their results are not stored)
+        const int64_t row = static_cast<int64_t>(q.tile.x) * p.d_out + n0;
+        const int4 rows = make_int4(static_cast<int>(row), static_cast<int>(row + 1), static_cast<int>(row + 4),
+                                    static_cast<int>(row + 5));
+        for (int u = lane >> 4; u < units; u += 2)
+          tma_gather4(b_ring + s * l.b_bytes + u * (kCols * 128) + group * 512, &map_b, u * 64, rows, &b_full[s]);
+      }
+    });
+  } else if (warp == 9) {
+    int nb = 0, ns = 0;
+    constexpr uint32_t idesc = idesc_f16_m64<E>(kCols);
+    for_pieces([&](const Piece& q) {
+      const int k = q.tile.w, kp = (k + 15) / 16 * 16;
+      if (k == 0) return;
+      wait_or_flag(&s_full, ns & 1, &abort_flag);
+      ++ns;
+      for (int b = 0; b < q.blocks; ++b, ++nb) {
+        const int s = nb % l.b_slots, d = nb & 1;
+        const uint32_t at = b_ring + s * l.b_bytes;
+        wait_or_flag(&b_full[s], (nb / l.b_slots) & 1, &abort_flag);
+        if (k < kp) {
+          // columns from k on are padding that may hold anything: the last step's become zero
+          for (int r = lane; r < kCols; r += 32)
+            for (int c = k; c < kp; ++c)
+              *reinterpret_cast<uint16_t*>(smem + (at - s_base) + (c >> 6) * (kCols * 128) + r * 128 +
+                                           ((((c & 63) >> 3) ^ (r & 7)) << 4) + (c & 7) * 2) = 0;
+          sm100::fence_proxy_async_smem();
+          __syncwarp();
         }
+        wait_or_flag(&d_empty[d], ((nb >> 1) & 1) ^ 1, &abort_flag);
+        sm100::tc_fence_after();
+        if (lane == 0) {
+          for (int t = 0; t < kT; ++t)
+            for (int ks = 0; ks < kp; ks += 16) {
+              const int pos_k = t * w.row_elems + ks;
+              tc_mma(tmem + d * kCols, s_base + (pos_k >> 6) * (kTile * 128) + (pos_k & 63) * 2,
+                     at + (ks >> 6) * (kCols * 128) + (ks & 63) * 2, idesc, t + ks > 0);
+            }
+          sm100::tc_commit(&b_empty[s]);
+          sm100::tc_commit(&d_full[d]);
+          if (b == q.blocks - 1) sm100::tc_commit(&s_empty);
+        }
+        __syncwarp();
       }
-    };
-    for (int s = 0; s < stages - 1; ++s) {
-      if (first + s < last) load(first + s);
-      cp_async_commit();
-    }
-    float up0 = 1.0f, up1 = 1.0f;
-    if (std::is_same<E, __half>::value && k) {
-      if (t0 >= 0) up0 = w.up[tile.y + r0];
-      if (t1 >= 0) up1 = w.up[tile.y + r1];
-    }
-    for (int block = first; block < last; ++block) {
-      if (stages == 3) cp_async_wait<1>();
-      else cp_async_wait<0>();
-      __syncthreads();
-      if (block + stages - 1 < last) load(block + stages - 1);
-      cp_async_commit();
-      if (wm * 16 >= count) continue;
-      const uint32_t at = ring + (block - first) % stages * stage_bytes;
-      float acc[4][4] = {};
-      auto step = [&](int ks) __attribute__((always_inline)) {
-        uint32_t q[2][4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          ldmatrix4(at + kSlots + (wn * 32 + j * 16 + (lane & 7) + ((lane >> 4) << 3)) * row_bytes +
-                        (2 * ks + ((lane >> 3) & 1)) * 16, q[j]);
-#pragma unroll
-        for (int t = 0; t < kT; ++t) {
-          uint32_t a[4];
-          ldmatrix4(s_base + (t * kTile + wm * 16 + (lane & 15)) * row_bytes + (2 * ks + (lane >> 4)) * 16, a);
+    });
+  } else {
+    const int wm = warp & 3, wn = warp >> 2, g = lane >> 2, c = lane & 3;
+    const bool in_place = p.y == p.y_in;
+    int nb = 0;
+    for_pieces([&](const Piece& q) {
+      const int k = q.tile.w, count = q.tile.z;
+      if (k == 0 && in_place) return;
+      const int r0 = wm * 16 + g, r1 = r0 + 8;
+      const int64_t t0 = r0 < count ? w.token[q.tile.y + r0] : -1, t1 = r1 < count ? w.token[q.tile.y + r1] : -1;
+      const int col = q.first * kCols + wn * 32 + c * 4;
+      const float* src0 = p.y_in ? p.y_in + t0 * p.y_in_stride + col : nullptr;
+      const float* src1 = p.y_in ? p.y_in + t1 * p.y_in_stride + col : nullptr;
+      float* dst0 = p.y + t0 * p.y_stride + col;
+      float* dst1 = p.y + t1 * p.y_stride + col;
+      auto fetch = [&](int b) {
+        if (p.y_in && b < q.blocks) {
+          const uint32_t slot = y_ring + b % l.y_slots * kSlot + tid * 16;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            mma16816<E>(acc[2 * j], a[0], a[1], a[2], a[3], q[j][0], q[j][1]);
-            mma16816<E>(acc[2 * j + 1], a[0], a[1], a[2], a[3], q[j][2], q[j][3]);
+            const int n = b * kCols + j * 16;
+            if (col + n >= p.d_out) continue;
+            if (t0 >= 0) cp_async16(slot + 2 * j * kAddThreads * 16, src0 + n, 16);
+            if (t1 >= 0) cp_async16(slot + (2 * j + 1) * kAddThreads * 16, src1 + n, 16);
           }
         }
+        cp_async_commit();
       };
-      if (units == 2 * KS) {                               // the pool's whole rank: a loop without tests
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) step(ks);
-      } else {
-        for (int ks = 0; ks < units / 2; ++ks) step(ks);
+      float up0 = 1.0f, up1 = 1.0f;
+      if (std::is_same<E, __half>::value && k) {
+        if (t0 >= 0) up0 = w.up[q.tile.y + r0];
+        if (t1 >= 0) up1 = w.up[q.tile.y + r1];
       }
-      const float4* slots = reinterpret_cast<const float4*>(smem + (at - s_base));
+      for (int b = 0; b < l.y_slots - 1; ++b) fetch(b);
+      for (int b = 0; b < q.blocks; ++b) {
+        fetch(b + l.y_slots - 1);                          // (into the slot that was read last)
+        if (l.y_slots == 4) cp_async_wait<3>();
+        else if (l.y_slots == 3) cp_async_wait<2>();
+        else cp_async_wait<1>();
+        float acc[4][4] = {};
+        if (k) {
+          const int d = nb & 1;
+          wait_or_flag(&d_full[d], (nb >> 1) & 1, &abort_flag);
+          ++nb;
+          if (wm * 16 < count) {
+            sm100::tc_fence_after();
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int n = block * kCols + wn * 32 + j * 16 + c * 4;
-        if (n >= p.d_out) continue;
-        float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = u;
-        if (p.y_in) {
-          u = slots[(2 * j) * kExpandThreads + tid];
-          v = slots[(2 * j + 1) * kExpandThreads + tid];
+            for (int j = 0; j < 4; ++j)
+              tmem_ld_16x8(tmem + (static_cast<uint32_t>(wm * 32) << 16) + d * kCols + wn * 32 + j * 8, acc[j]);
+            sm100::tmem_ld_wait();
+            sm100::tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) sm100::mbar_arrive(&d_empty[d]);
         }
-        if (t0 >= 0)
-          __stcs(reinterpret_cast<float4*>(p.y + t0 * p.y_stride + n),
-                 make_float4(fmaf(acc[2 * j][0], up0, u.x), fmaf(acc[2 * j][1], up0, u.y),
-                             fmaf(acc[2 * j + 1][0], up0, u.z), fmaf(acc[2 * j + 1][1], up0, u.w)));
-        if (t1 >= 0)
-          __stcs(reinterpret_cast<float4*>(p.y + t1 * p.y_stride + n),
-                 make_float4(fmaf(acc[2 * j][2], up1, v.x), fmaf(acc[2 * j][3], up1, v.y),
-                             fmaf(acc[2 * j + 1][2], up1, v.z), fmaf(acc[2 * j + 1][3], up1, v.w)));
+        const float4* slots = reinterpret_cast<const float4*>(smem + (y_ring - s_base) + b % l.y_slots * kSlot) + tid;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int n = b * kCols + j * 16;
+          if (col + n >= p.d_out) continue;
+          float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = u;
+          if (p.y_in) {
+            u = slots[2 * j * kAddThreads];
+            v = slots[(2 * j + 1) * kAddThreads];
+          }
+          if (t0 >= 0)
+            __stcs(reinterpret_cast<float4*>(dst0 + n),
+                   make_float4(fmaf(acc[2 * j][0], up0, u.x), fmaf(acc[2 * j][1], up0, u.y),
+                               fmaf(acc[2 * j + 1][0], up0, u.z), fmaf(acc[2 * j + 1][1], up0, u.w)));
+          if (t1 >= 0)
+            __stcs(reinterpret_cast<float4*>(dst1 + n),
+                   make_float4(fmaf(acc[2 * j][2], up1, v.x), fmaf(acc[2 * j][3], up1, v.y),
+                               fmaf(acc[2 * j + 1][2], up1, v.z), fmaf(acc[2 * j + 1][3], up1, v.w)));
+        }
       }
-    }
+    });
   }
+  sm100::tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    sm100::tc_fence_after();
+    sm100::tmem_dealloc(tmem, 2 * kCols);
+  }
+  if (tid == 0 && *static_cast<volatile int*>(&abort_flag)) report_timeout();
 }
 
-template <typename E, int NB>
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn get_encode() {
+  static EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// A 16-bit matrix [rows, cols], in boxes of 64 columns x box_rows with the 128-byte swizzle.
+template <typename E>
+bool tensor_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t stride, int box_rows) {
+  EncodeFn enc = get_encode();
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)}, estr[2] = {1, 1};
+  return enc && enc(map, std::is_same<E, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                    2, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename E, int R>
 int launch_shrink(const LoraArgs& p, const Work& w, int64_t tiles, int sms, cudaStream_t st) {
-  constexpr int smem = shrink_smem<NB>();
-  auto kern = lora_shrink_kernel<E, NB>;
+  constexpr int smem = Shrink<R>::kSmem;
+  auto kern = lora_shrink_kernel<E, R>;
   static std::atomic<uint64_t> done{0};
   if (set_smem_once(kern, smem, done) != WUSH_OK) return WUSH_ERR_CUDA;
   // Split d_in so that the tiles' clusters fill the SMs once, but not below 256 columns a
   // CTA (the number of tiles is known on the device only: the runs' ends are taken as half
   // a tile each).
-  constexpr int kFit = 227 * 1024 / (smem + 1024), kCtas = NB > 8 ? 1 : kFit < 3 ? kFit : 3;
   const int64_t likely = (p.tokens + kTile - 1) / kTile + (p.n_adapters < p.tokens ? p.n_adapters : p.tokens) / 2;
-  int64_t splits = kCtas * sms / likely;
-  if (splits > p.d_in / 256) splits = p.d_in / 256;
-  splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
+  // (A cluster lies within one of the GPU's eight GPCs.)
+  const int64_t gpc = sms / 8 * Shrink<R>::kCtas;
+  int64_t splits = 8;
+  while (splits > 1 && (gpc / splits * 8 < likely || splits > p.d_in / 256)) --splits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
   cfg.blockDim = dim3(kShrinkThreads);
@@ -776,22 +1103,29 @@ int launch_shrink(const LoraArgs& p, const Work& w, int64_t tiles, int sms, cuda
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, kern, p, w) != cudaSuccess) return WUSH_ERR_CUDA;
+  CUtensorMap map_x, map_x8, map_a;
+  if (!tensor_map<E>(&map_x, p.x, p.tokens, p.d_in, p.x_stride, 1) ||
+      !tensor_map<E>(&map_x8, p.x, p.tokens, p.d_in, p.x_stride, 8) ||
+      !tensor_map<E>(&map_a, p.a, int64_t(p.n_adapters) * p.rank, p.d_in, p.d_in, R))
+    return WUSH_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, p, w, map_x, map_x8, map_a) != cudaSuccess) return WUSH_ERR_CUDA;
   return launch_status();
 }
 
-template <typename E, int KS>
+template <typename E>
 int launch_expand(const LoraArgs& p, const Work& w, int64_t tiles, int sms, cudaStream_t st) {
-  // three stages of the ring where two CTAs an SM hold them, else two
-  const int row_bytes = w.row_elems * 2 + 16, terms = Split<E>::kTerms * kTile * row_bytes;
-  const int stage = kTile * kCols * 4 + kCols * row_bytes;
-  const int stages = terms + 3 * stage <= 111 * 1024 ? 3 : 2, smem = terms + stages * stage;
-  auto kern = lora_expand_kernel<E, KS>;
+  const Expand l = expand_layout<E>(w.row_elems);
+  auto kern = lora_expand_kernel<E>;
   static std::atomic<uint64_t> done{0};
   if (set_smem_once(kern, kMaxSmem, done) != WUSH_OK) return WUSH_ERR_CUDA;
-  const int fit = 227 * 1024 / (smem + 1024), ctas = fit < 1 ? 1 : fit < 3 ? fit : 3;
-  const int64_t blocks = (p.d_out + kCols - 1) / kCols, slots = int64_t(sms) * ctas, items = tiles * ((blocks + 1) / 2);
-  return launch_pdl(kern, static_cast<unsigned>(items < slots ? items : slots), kExpandThreads, smem, st, p, w, stages, 16);
+  const int64_t blocks = (p.d_out + kCols - 1) / kCols, items = tiles * blocks;
+  const int64_t slots = int64_t(sms) * (l.smem <= kMaxSmem / 2 ? 2 : 1);
+  CUtensorMap map_s, map_b;
+  if (!tensor_map<E>(&map_s, w.terms, p.tokens, Split<E>::kTerms * w.row_elems, Split<E>::kTerms * w.row_elems, kTile) ||
+      !tensor_map<E>(&map_b, p.b, int64_t(p.n_adapters) * p.d_out, p.rank, p.rank, 1))
+    return WUSH_ERR_CUDA;
+  return launch_pdl(kern, static_cast<unsigned>(items < slots ? items : slots), kExpandThreads, l.smem, st, p, w, l, map_s,
+                    map_b);
 }
 
 template <typename E>
@@ -801,40 +1135,36 @@ int launch_many(const LoraArgs& p, const Work& w, cudaStream_t st) {
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return WUSH_ERR_CUDA;
   const int64_t tiles = max_tiles(p.tokens, p.n_adapters);
-  const int plan_smem = (p.n_adapters + 1) * 4;
+  const bool ordered = p.n_adapters <= kOrderedAdapters;
+  const int plan_smem = (p.n_adapters + 1) * 4 * (ordered ? 32 : 1);
+  auto plan = ordered ? lora_plan_kernel<true> : lora_plan_kernel<false>;
   if (plan_smem > 48 * 1024 - 256) {
-    static std::atomic<uint64_t> done{0};
-    if (set_smem_once(lora_plan_kernel, (kPlanAdapters + 1) * 4, done) != WUSH_OK) return WUSH_ERR_CUDA;
+    static std::atomic<uint64_t> done[2] = {{0}, {0}};
+    const int most = ordered ? (kOrderedAdapters + 1) * 128 : (kPlanAdapters + 1) * 4;
+    if (set_smem_once(plan, most, done[ordered]) != WUSH_OK) return WUSH_ERR_CUDA;
   }
-  int rc = launch_pdl(lora_plan_kernel, 1, kPlanThreads, plan_smem, st, p.adapter, p.tokens, p.n_adapters, p.rank,
-                      p.ranks, w);
+  int rc = launch_pdl(plan, 1, kPlanThreads, plan_smem, st, p.adapter, p.tokens, p.n_adapters, p.rank, p.ranks, w);
   if (rc != WUSH_OK) return rc;
-  rc = p.rank <= 16    ? launch_shrink<E, 2>(p, w, tiles, sms, st)
-       : p.rank <= 32  ? launch_shrink<E, 4>(p, w, tiles, sms, st)
-       : p.rank <= 64  ? launch_shrink<E, 8>(p, w, tiles, sms, st)
-       : p.rank <= 128 ? launch_shrink<E, 16>(p, w, tiles, sms, st)
-                       : launch_shrink<E, 32>(p, w, tiles, sms, st);
+  rc = p.rank <= 16    ? launch_shrink<E, 16>(p, w, tiles, sms, st)
+       : p.rank <= 32  ? launch_shrink<E, 32>(p, w, tiles, sms, st)
+       : p.rank <= 64  ? launch_shrink<E, 64>(p, w, tiles, sms, st)
+       : p.rank <= 128 ? launch_shrink<E, 128>(p, w, tiles, sms, st)
+                       : launch_shrink<E, 256>(p, w, tiles, sms, st);
   if (rc != WUSH_OK) return rc;
-  switch (w.row_elems) {
-    case 16: return launch_expand<E, 1>(p, w, tiles, sms, st);
-    case 32: return launch_expand<E, 2>(p, w, tiles, sms, st);
-    case 48: return launch_expand<E, 3>(p, w, tiles, sms, st);
-    case 64: return launch_expand<E, 4>(p, w, tiles, sms, st);
-    default: return launch_expand<E, 8>(p, w, tiles, sms, st);
-  }
+  return launch_expand<E>(p, w, tiles, sms, st);
 }
 
-// Few tokens (or a pool too large to count in shared memory) go through the cluster
-// kernel, whose clusters each look through the adapters of all tokens.
+// Few tokens (or a pool too large to count in shared memory, or for a tensor map) go through
+// the cluster kernel, whose clusters each look through the adapters of all tokens.
 constexpr int kFewTokens = 256;
 
-bool few(int64_t tokens, int64_t n) {
-  static const int f = getenv("FEW") ? atoi(getenv("FEW")) : kFewTokens;
-  return tokens <= f || n > kPlanAdapters; }
+bool few(int64_t tokens, int64_t n, int64_t d_out) {
+  return tokens <= kFewTokens || n > kPlanAdapters || n * d_out > 0x7fffffff;
+}
 
 template <typename E>
 int run_lora(const LoraArgs& p, void* workspace, cudaStream_t st) {
-  if (!few(p.tokens, p.n_adapters)) {
+  if (!few(p.tokens, p.n_adapters, p.d_out)) {
     Work w;
     work_layout(p.tokens, p.n_adapters, p.rank, static_cast<char*>(workspace), &w);
     return launch_many<E>(p, w, st);
@@ -861,7 +1191,7 @@ using namespace wush;
 extern "C" size_t wush_lora_workspace_bytes(int64_t tokens, int64_t d_in, int64_t d_out, int64_t n_adapters,
                                             int64_t rank) {
   if (!sizes_ok(tokens, d_in, d_out, n_adapters, rank) || !sizes_taken(tokens, d_in, d_out, n_adapters, rank) ||
-      few(tokens, n_adapters))
+      few(tokens, n_adapters, d_out))
     return 0;
   return work_layout(tokens, n_adapters, rank, nullptr, nullptr);
 }

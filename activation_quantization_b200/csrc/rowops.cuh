@@ -11,8 +11,10 @@
 
 namespace wush {
 
-// Error word of the kernels with bounded waits in block_norm.cu (see common.cuh).
+// Error words of the kernels with bounded waits in block_norm.cu and lora.cu (see
+// common.cuh).
 int read_and_clear_norm_error(int* word);
+int read_and_clear_lora_error(int* word);
 
 inline int dtype_bytes(int dt) { return dt == WUSH_FP32 ? 4 : 2; }
 inline bool known_dtype(int dt) { return dt == WUSH_BF16 || dt == WUSH_FP32 || dt == WUSH_FP16; }
