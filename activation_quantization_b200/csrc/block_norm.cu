@@ -62,6 +62,7 @@ struct Args {
   int64_t rows;
   int d, row_threads;                                      // threads of one row (a multiple of 32)
   float inv_d;
+  int phase, phase_step;                                   // kShifted: row i begins (phase + i phase_step) % 4 behind a quad
 };
 
 // Where the ring kernel keeps things (bytes from the start of its shared memory; -1:
@@ -110,11 +111,11 @@ struct Vectors {
 };
 
 // v = N(v) over the row.
-template <bool VEC, int NV>
+template <int MODE, int NV>
 __device__ __forceinline__ void apply_norm(const Args& a, const NormArgs& n, const Vectors& vec, float (&v)[NV][8],
-                                           float (*red)[32], int g, int tid, int warp0, int d) {
+                                           float (*red)[32], const Columns<MODE>& q, int warp0) {
   if (n.kind == WUSH_ROWNORM_NONE) return;
-  const int warps = g >> 5;
+  const int warps = q.g >> 5;
   float s = 0.0f;
   if (n.kind == WUSH_ROWNORM_LAYER) {
 #pragma unroll
@@ -125,7 +126,7 @@ __device__ __forceinline__ void apply_norm(const Args& a, const NormArgs& n, con
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[j][e] = group_column<VEC>(j, e, g, tid) < d ? v[j][e] - mean : 0.0f;
+      for (int e = 0; e < 8; ++e) v[j][e] = q.has(q.at(j, e)) ? v[j][e] - mean : 0.0f;
   }
   float2 sq = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -135,7 +136,7 @@ __device__ __forceinline__ void apply_norm(const Args& a, const NormArgs& n, con
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float x[8];
-      load_group<WUSH_FP32, VEC>(vec.w, j, g, tid, d, x);
+      load_group<WUSH_FP32, MODE>(vec.w, j, q, x);
       scale8(v[j], f);
       mul8(v[j], x);
     }
@@ -144,7 +145,7 @@ __device__ __forceinline__ void apply_norm(const Args& a, const NormArgs& n, con
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float x[8];
-        load_group<dt.value, VEC>(n.w, j, g, tid, d, x);
+        load_group<dt.value, MODE, true>(n.w, j, q, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] += n.offset;
         scale8(v[j], f);
@@ -159,7 +160,7 @@ __device__ __forceinline__ void apply_norm(const Args& a, const NormArgs& n, con
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float x[8];
-      load_group<WUSH_FP32, VEC>(vec.b, j, g, tid, d, x);
+      load_group<WUSH_FP32, MODE>(vec.b, j, q, x);
       add8(v[j], x);
     }
   } else if (n.b) {
@@ -167,39 +168,41 @@ __device__ __forceinline__ void apply_norm(const Args& a, const NormArgs& n, con
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float x[8];
-        load_group<dt.value, VEC>(n.b, j, g, tid, d, x);
+        load_group<dt.value, MODE, true>(n.b, j, q, x);
         add8(v[j], x);
       }
     });
   }
 }
 
-template <bool VEC, int NV>
-__device__ __forceinline__ void load_row(const void* row, int dt, int g, int tid, int d, float (&v)[NV][8]) {
+template <int MODE, int NV>
+__device__ __forceinline__ void load_row(const void* row, int dt, const Columns<MODE>& q, float (&v)[NV][8]) {
   with_dtype(dt, [&](auto t) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load_group<t.value, VEC>(row, j, g, tid, d, v[j]);
+    for (int j = 0; j < NV; ++j) load_group<t.value, MODE>(row, j, q, v[j]);
   });
 }
 
-template <bool VEC, int NV>
-__device__ __forceinline__ void store_row(void* row, int dt, int g, int tid, int d, const float (&v)[NV][8]) {
+template <int MODE, int NV>
+__device__ __forceinline__ void store_row(void* row, int dt, const Columns<MODE>& q, const float (&v)[NV][8]) {
   with_dtype(dt, [&](auto t) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) store_group<t.value, VEC>(row, j, g, tid, d, v[j]);
+    for (int j = 0; j < NV; ++j) store_group<t.value, MODE>(row, j, q, v[j]);
   });
 }
 
-// v = residual_scale * r + branch_scale * v * act(gate)
-template <bool VEC, int NV>
-__device__ __forceinline__ void gate_and_add(const Args& a, const void* gate, int gate_dt, const void* r, float (&v)[NV][8], int g,
-                                             int tid, int d) {
+// v = residual_scale * r + branch_scale * v * act(gate).  ``loose``: the gate is a vector in
+// the caller's memory.
+template <int MODE, int NV>
+__device__ __forceinline__ void gate_and_add(const Args& a, const void* gate, int gate_dt, bool loose, const void* r,
+                                             float (&v)[NV][8], const Columns<MODE>& q) {
   if (gate)
     with_dtype(gate_dt, [&](auto t) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float x[8];
-        load_group<t.value, VEC>(gate, j, g, tid, d, x);
+        if (MODE == kShifted && loose) load_group<t.value, MODE, true>(gate, j, q, x);
+        else load_group<t.value, MODE>(gate, j, q, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[j][e] *= activate(x[e], a.act);
       }
@@ -209,7 +212,7 @@ __device__ __forceinline__ void gate_and_add(const Args& a, const void* gate, in
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float x[8];
-        load_group<t.value, VEC>(r, j, g, tid, d, x);
+        load_group<t.value, MODE>(r, j, q, x);
         blend8(v[j], a.branch_scale, x, a.residual_scale);
       }
     });
@@ -222,29 +225,28 @@ __device__ __forceinline__ void gate_and_add(const Args& a, const void* gate, in
 // ---------------------------------------------------------------------------
 // Few rows: one CTA a row (narrow rows share one).
 // ---------------------------------------------------------------------------
-template <bool VEC>
+template <int MODE>
 __global__ void __launch_bounds__(1024) norm_few_kernel(const __grid_constant__ Args a) {
   __shared__ __align__(16) float red[4][32];
   const int g = a.row_threads, sub = threadIdx.x / g, tid = threadIdx.x - sub * g, warp0 = sub * (g >> 5);
   const int64_t row = int64_t(blockIdx.x) * (blockDim.x / g) + sub;
   const bool live = row < a.rows;                          // the others only take part in the barriers
-  const int d = live ? a.d : 0;
+  const Columns<MODE> q = {g, tid, live ? a.d : 0, 0};
   float v[1][8];
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
   const void* r = a.r ? row_of(a.r, a.r_dt, row * a.r_stride) : nullptr;
   if (a.y) {
-    load_row<VEC, 1>(row_of(a.y, a.y_dt, row * a.y_stride), a.y_dt, g, tid, d, v);
-    apply_norm<VEC, 1>(a, a.post, Vectors{}, v, red, g, tid, warp0, d);
-    gate_and_add<VEC, 1>(a, a.gate ? row_of(a.gate, a.gate_dt, row * a.gate_stride) : nullptr, a.gate_dt,
-                         r, v, g, tid, d);
-    if (a.r_out) store_row<VEC, 1>(row_of(a.r_out, a.r_dt, row * a.r_out_stride), a.r_dt, g, tid, d, v);
+    load_row<MODE, 1>(row_of(a.y, a.y_dt, row * a.y_stride), a.y_dt, q, v);
+    apply_norm<MODE, 1>(a, a.post, Vectors{}, v, red, q, warp0);
+    gate_and_add<MODE, 1>(a, a.gate ? row_of(a.gate, a.gate_dt, row * a.gate_stride) : nullptr, a.gate_dt, false, r, v, q);
+    if (a.r_out) store_row<MODE, 1>(row_of(a.r_out, a.r_dt, row * a.r_out_stride), a.r_dt, q, v);
   } else {
-    load_row<VEC, 1>(r, a.r_dt, g, tid, d, v);
+    load_row<MODE, 1>(r, a.r_dt, q, v);
   }
   if (a.h) {
-    apply_norm<VEC, 1>(a, a.pre, Vectors{}, v, red + 2, g, tid, warp0, d);
-    store_row<VEC, 1>(row_of(a.h, a.h_dt, row * a.h_stride), a.h_dt, g, tid, d, v);
+    apply_norm<MODE, 1>(a, a.pre, Vectors{}, v, red + 2, q, warp0);
+    store_row<MODE, 1>(row_of(a.h, a.h_dt, row * a.h_stride), a.h_dt, q, v);
   }
 }
 
@@ -252,16 +254,15 @@ __global__ void __launch_bounds__(1024) norm_few_kernel(const __grid_constant__ 
 // Many rows: a ring of rows in shared memory.
 //
 // A stage of a tensor holds one row at the 16-byte phase that the row has in global
-// memory.  The whole 16-byte units of the row come by a bulk copy; what is left at its
-// ends when rows are not aligned (VEC false) is copied by single threads.  y has a
+// memory, so that a bulk copy of the 16-byte units that it touches brings it.  y has a
 // barrier of its own, r and the gate share one: y's stage is refilled as soon as the
 // first reduction has read it, the others' after the second.
 // ---------------------------------------------------------------------------
-// CTAs an SM: 64 registers a thread.
-constexpr int ring_ctas(int g) { return 1024 / g; }
+// CTAs an SM: 64 registers a thread, 80 where a thread of 256 has more than 16 elements.
+constexpr int ring_ctas(int nv, int g) { return g == 256 && nv > 2 ? 3 : 1024 / g; }
 
-template <bool VEC, int NV, int G>
-__global__ void __launch_bounds__(G, ring_ctas(G)) norm_ring_kernel(const __grid_constant__ Args a,
+template <int MODE, int NV, int G>
+__global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __grid_constant__ Args a,
                                                          const __grid_constant__ Ring q) {
   extern __shared__ __align__(128) char smem[];
   __shared__ __align__(16) float red[2][4][32];
@@ -269,6 +270,8 @@ __global__ void __launch_bounds__(G, ring_ctas(G)) norm_ring_kernel(const __grid
   __shared__ int abort_flag;
   constexpr int g = G;                                     // (a constant, so that columns are immediate offsets)
   const int tid = threadIdx.x, d = a.d;
+  // (a CTA's rows are gridDim.x apart, a multiple of four, and so all have one shift)
+  const Columns<MODE> cols = {g, tid, d, MODE == kShifted ? (a.phase + (blockIdx.x & 3) * a.phase_step) & 3 : 0};
   const bool gate_rows = a.gate && a.gate_stride;
   const int n_rows = static_cast<int>((a.rows - 1 - blockIdx.x) / gridDim.x) + 1;   // (at most one CTA a row)
 
@@ -283,10 +286,10 @@ __global__ void __launch_bounds__(G, ring_ctas(G)) norm_ring_kernel(const __grid
   for (int i = tid; i < 2 * 4 * 32; i += g) (&red[0][0][0])[i] = 0.0f;
   sm100::pdl_wait();                                       // nothing global is touched before this
   sm100::pdl_launch_dependents();
-  // the vectors that every row uses, as fp32
+  // the vectors that every row uses, as fp32 and shifted like the rows
   auto stage = [&](const void* p, int dt, int at, float offset) -> const float* {
     if (!p || at < 0) return nullptr;
-    float* out = reinterpret_cast<float*>(smem + at);
+    float* out = reinterpret_cast<float*>(smem + at) + cols.shift;
     with_dtype(dt, [&](auto t) __attribute__((always_inline)) {
       for (int i = tid; i < d; i += g) out[i] = load1<t.value>(p, i) + offset;
     });
@@ -299,24 +302,39 @@ __global__ void __launch_bounds__(G, ring_ctas(G)) norm_ring_kernel(const __grid
   const float* gate_vec = gate_rows ? nullptr : stage(a.gate, a.gate_dt, q.vec[4], 0.0f);
   __syncthreads();
 
-  // One row of one tensor into its stage: its whole 16-byte units by a bulk copy (thread 0;
-  // ``units`` gives their first byte and their number of bytes) and, by the first warp, the
-  // elements at its ends.
-  auto units = [&](int64_t at, int size, int64_t* lo) {
-    const int64_t end = at + int64_t(d) * size, hi = VEC ? end : end & ~int64_t(15);
-    *lo = VEC ? at : (at + 15) & ~int64_t(15);
+  // One row of one tensor into its stage, by a bulk copy (thread 0) of the 16-byte units that
+  // it touches: ``units`` gives their first byte and their number of bytes.  What a unit holds
+  // beside the row is never used.  Units that reach beyond the matrix (its first row's first,
+  // its last row's last) are left out, and the first warp copies the elements there.
+  struct Bounds {
+    int64_t lo, hi;                                        // the matrix's whole units
+  };
+  auto bounds = [&](const void* p, int dt, int64_t stride) {
+    const int64_t at = reinterpret_cast<int64_t>(p);
+    return Bounds{(at + 15) & ~int64_t(15),
+                  reinterpret_cast<int64_t>(row_of(p, dt, (a.rows - 1) * stride + d)) & ~int64_t(15)};
+  };
+  auto units = [&](int64_t at, int size, const Bounds& m, int64_t* lo) {
+    const int64_t end = at + int64_t(d) * size;
+    if (MODE == kAligned) {
+      *lo = at;
+      return static_cast<uint32_t>(end - at);
+    }
+    const int64_t from = at & ~int64_t(15), to = (end + 15) & ~int64_t(15), hi = to < m.hi ? to : m.hi;
+    *lo = from > m.lo ? from : m.lo;
     return hi > *lo ? static_cast<uint32_t>(hi - *lo) : 0u;
   };
-  auto bulk = [&](int64_t at, int size, char* to, uint64_t* bar) {
+  auto bulk = [&](int64_t at, int size, const Bounds& m, char* to, uint64_t* bar) {
     int64_t lo;
-    const uint32_t bytes = units(at, size, &lo);
+    const uint32_t bytes = units(at, size, m, &lo);
     if (bytes) sm100::bulk_load(to + (at & 15) + (lo - at), reinterpret_cast<const void*>(lo), bytes, bar);
   };
-  auto ends = [&](int64_t at, int size, char* to) {
+  auto ends = [&](int64_t at, int size, const Bounds& m, char* to) {
     int64_t lo;
-    const uint32_t bytes = units(at, size, &lo);
-    const int head = bytes ? static_cast<int>(lo - at) / size : d;          // elements before the units
-    const int tail = bytes ? static_cast<int>(lo + bytes - at) / size : d;  // first element behind them
+    const uint32_t bytes = units(at, size, m, &lo);
+    const int64_t hi = lo + bytes, end = at + int64_t(d) * size;
+    const int head = !bytes ? d : lo > at ? static_cast<int>(lo - at) / size : 0;       // elements before the units
+    const int tail = !bytes ? d : hi < end ? static_cast<int>(hi - at) / size : d;      // first element behind them
     for (int i = tid; i < head + (d - tail); i += 32) {
       const int e = (i < head ? i : tail + i - head) * size;
       char* dst = to + (at & 15) + e;
@@ -324,6 +342,8 @@ __global__ void __launch_bounds__(G, ring_ctas(G)) norm_ring_kernel(const __grid
       else *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(at + e);
     }
   };
+  const Bounds in_y = bounds(a.y, a.y_dt, a.y_stride), in_r = bounds(a.r, a.r_dt, a.r_stride),
+               in_g = bounds(a.gate, a.gate_dt, a.gate_stride);
   auto address = [&](const void* p, int dt, int64_t stride, int i) {       // of the CTA's row i
     return reinterpret_cast<int64_t>(row_of(p, dt, (blockIdx.x + int64_t(i) * gridDim.x) * stride));
   };
@@ -331,31 +351,31 @@ __global__ void __launch_bounds__(G, ring_ctas(G)) norm_ring_kernel(const __grid
   const int y_size = a.y_dt == WUSH_FP32 ? 4 : 2, r_size = a.r_dt == WUSH_FP32 ? 4 : 2,
             gate_size = a.gate_dt == WUSH_FP32 ? 4 : 2;
   auto fill_y = [&](int i, int s) {                        // the CTA's row i into stage s
-    if (!a.y || i >= n_rows || tid >= (VEC ? 1 : 32)) return;
+    if (!a.y || i >= n_rows || tid >= (MODE == kAligned ? 1 : 32)) return;
     const int64_t at = address(a.y, a.y_dt, a.y_stride, i);
     char* to = smem + q.y + s * q.y_step;
     if (tid == 0) {
       int64_t lo;
-      sm100::mbar_arrive_expect_tx(&full[0][s], units(at, y_size, &lo));
-      bulk(at, y_size, to, &full[0][s]);
+      sm100::mbar_arrive_expect_tx(&full[0][s], units(at, y_size, in_y, &lo));
+      bulk(at, y_size, in_y, to, &full[0][s]);
     }
-    if (!VEC) ends(at, y_size, to);
+    if (MODE != kAligned) ends(at, y_size, in_y, to);
   };
   auto fill_rest = [&](int i, int s) {
-    if (i >= n_rows || tid >= (VEC ? 1 : 32)) return;
+    if (i >= n_rows || tid >= (MODE == kAligned ? 1 : 32)) return;
     const int64_t at_r = r_ring ? address(a.r, a.r_dt, a.r_stride, i) : 0;
     const int64_t at_g = gate_ring ? address(a.gate, a.gate_dt, a.gate_stride, i) : 0;
     char* to_r = smem + q.r + s * q.r_step;
     char* to_g = smem + q.gate + s * q.gate_step;
     if (tid == 0) {
       int64_t lo;
-      sm100::mbar_arrive_expect_tx(&full[1][s], (r_ring ? units(at_r, r_size, &lo) : 0u) +
-                                                    (gate_ring ? units(at_g, gate_size, &lo) : 0u));
-      if (r_ring) bulk(at_r, r_size, to_r, &full[1][s]);
-      if (gate_ring) bulk(at_g, gate_size, to_g, &full[1][s]);
+      sm100::mbar_arrive_expect_tx(&full[1][s], (r_ring ? units(at_r, r_size, in_r, &lo) : 0u) +
+                                                    (gate_ring ? units(at_g, gate_size, in_g, &lo) : 0u));
+      if (r_ring) bulk(at_r, r_size, in_r, to_r, &full[1][s]);
+      if (gate_ring) bulk(at_g, gate_size, in_g, to_g, &full[1][s]);
     }
-    if (!VEC && r_ring) ends(at_r, r_size, to_r);
-    if (!VEC && gate_ring) ends(at_g, gate_size, to_g);
+    if (MODE != kAligned && r_ring) ends(at_r, r_size, in_r, to_r);
+    if (MODE != kAligned && gate_ring) ends(at_g, gate_size, in_g, to_g);
   };
   // (a wait that gives up marks the error and lets the CTA run on, so that its barriers
   // stay uniform; every later wait then gives up at once)
@@ -379,14 +399,14 @@ __global__ void __launch_bounds__(G, ring_ctas(G)) norm_ring_kernel(const __grid
     float v[NV][8];
     // a row lies in its stage at the 16-byte phase that it has in global memory
     auto phase = [&](const void* p, int dt, int64_t stride) {
-      return VEC ? 0 : static_cast<int>(reinterpret_cast<int64_t>(row_of(p, dt, row * stride)) & 15);
+      return MODE == kAligned ? 0 : static_cast<int>(reinterpret_cast<int64_t>(row_of(p, dt, row * stride)) & 15);
     };
     const char* r_stage = smem + q.r + s * q.r_step + phase(a.r, a.r_dt, a.r_stride);
-    if (!VEC) __syncthreads();                             // the rows' ends are in place
+    if (MODE != kAligned) __syncthreads();                             // the rows' ends are in place
     if (a.y) {
       wait(&full[0][s], parity);
-      load_row<VEC, NV>(smem + q.y + s * q.y_step + phase(a.y, a.y_dt, a.y_stride), a.y_dt, g, tid, d, v);
-      apply_norm<VEC, NV>(a, a.post, post, v, sums, g, tid, 0, d);
+      load_row<MODE, NV>(smem + q.y + s * q.y_step + phase(a.y, a.y_dt, a.y_stride), a.y_dt, cols, v);
+      apply_norm<MODE, NV>(a, a.post, post, v, sums, cols, 0);
       if (a.post.kind == WUSH_ROWNORM_NONE) __syncthreads();
       fill_y(i + q.stages, s);
       wait(&full[1][s], parity);
@@ -395,17 +415,17 @@ __global__ void __launch_bounds__(G, ring_ctas(G)) norm_ring_kernel(const __grid
       if (gate_ring) gate = smem + q.gate + s * q.gate_step + phase(a.gate, a.gate_dt, a.gate_stride);
       else if (gate_vec) gate = gate_vec, gate_dt = WUSH_FP32;
       else if (a.gate) gate = row_of(a.gate, a.gate_dt, row * a.gate_stride);
-      gate_and_add<VEC, NV>(a, gate, gate_dt,
-                            r_ring ? r_stage : a.r ? row_of(a.r, a.r_dt, row * a.r_stride) : nullptr, v, g, tid, d);
-      if (a.r_out) store_row<VEC, NV>(row_of(a.r_out, a.r_dt, row * a.r_out_stride), a.r_dt, g, tid, d, v);
+      gate_and_add<MODE, NV>(a, gate, gate_dt, !gate_rows && !gate_vec,
+                             r_ring ? r_stage : a.r ? row_of(a.r, a.r_dt, row * a.r_stride) : nullptr, v, cols);
+      if (a.r_out) store_row<MODE, NV>(row_of(a.r_out, a.r_dt, row * a.r_out_stride), a.r_dt, cols, v);
     } else {
       wait(&full[1][s], parity);
-      load_row<VEC, NV>(r_stage, a.r_dt, g, tid, d, v);
+      load_row<MODE, NV>(r_stage, a.r_dt, cols, v);
     }
-    if (a.h) apply_norm<VEC, NV>(a, a.pre, pre, v, sums + 2, g, tid, 0, d);
+    if (a.h) apply_norm<MODE, NV>(a, a.pre, pre, v, sums + 2, cols, 0);
     if (!a.h || a.pre.kind == WUSH_ROWNORM_NONE) __syncthreads();
     fill_rest(i + q.stages, s);
-    if (a.h) store_row<VEC, NV>(row_of(a.h, a.h_dt, row * a.h_stride), a.h_dt, g, tid, d, v);
+    if (a.h) store_row<MODE, NV>(row_of(a.h, a.h_dt, row * a.h_stride), a.h_dt, cols, v);
     if (++s == q.stages) s = 0, parity ^= 1;
   }
   if (gave_up) {
@@ -459,11 +479,11 @@ constexpr int kInFlight = 96 * 1024;                       // bytes of rows that
 // up to four.  Measured at 4096 rows x 4096 (fp32 y, bf16 stream): four CTAs of 256
 // threads with one stage 30.7 us, two with two stages 34.4 us, eight of 128 threads 32.5 us;
 // at 8192 x 5120 bf16: 32.1 us with two stages, 36.6 us with one.
-int plan(const Args& a, bool vec, int ctas, Ring* q) {
+int plan(const Args& a, bool aligned, int ctas, Ring* q) {
   const int budget = kSmemPerSm / ctas - kCtaOverhead;
   auto up = [](int64_t n) { return static_cast<int>((n + 15) / 16 * 16); };
   const bool gate_rows = a.gate && a.gate_stride;
-  const int edge = vec ? 0 : 16;                           // rows keep their 16-byte phase
+  const int edge = aligned ? 0 : 16;                           // rows keep their 16-byte phase
   const int y = a.y ? up(int64_t(a.d) * dtype_bytes(a.y_dt) + edge) : 0;
   int r = a.r ? up(int64_t(a.d) * dtype_bytes(a.r_dt) + edge) : 0;
   int gate = gate_rows ? up(int64_t(a.d) * dtype_bytes(a.gate_dt) + edge) : 0;
@@ -475,7 +495,7 @@ int plan(const Args& a, bool vec, int ctas, Ring* q) {
   if (q->stages > kMaxStages) q->stages = kMaxStages;
   const void* vecs[5] = {a.post.w, a.post.b, a.pre.w, a.pre.b, gate_rows ? nullptr : a.gate};
   int all = 0;
-  for (int k = 0; k < 5; ++k) all += vecs[k] ? up(int64_t(a.d) * 4) : 0;
+  for (int k = 0; k < 5; ++k) all += vecs[k] ? up(int64_t(a.d) * 4 + edge) : 0;
   q->kept = all + q->stages * stage <= budget;             // otherwise they are read from L2, row by row
   int at = 0;
   q->y = at; q->y_step = y; at += y * q->stages;
@@ -483,34 +503,56 @@ int plan(const Args& a, bool vec, int ctas, Ring* q) {
   q->gate = gate ? at : -1; q->gate_step = gate; at += gate * q->stages;
   for (int k = 0; k < 5; ++k) {
     q->vec[k] = q->kept && vecs[k] ? at : -1;
-    if (q->vec[k] >= 0) at += up(int64_t(a.d) * 4);
+    if (q->vec[k] >= 0) at += up(int64_t(a.d) * 4 + edge);
   }
   return at;
 }
 
-template <bool VEC, int NV, int G>
+template <int MODE, int NV, int G>
 int launch_ring(const Args& a, int sms, cudaStream_t st) {
   Ring q = {};
-  const int ctas = ring_ctas(G), smem = plan(a, VEC, ctas, &q);
-  auto kern = norm_ring_kernel<VEC, NV, G>;
+  const int ctas = ring_ctas(NV, G), smem = plan(a, MODE == kAligned, ctas, &q);
+  auto kern = norm_ring_kernel<MODE, NV, G>;
   static std::atomic<uint64_t> done{0};
   if (set_smem_once(kern, kSmemPerSm, done) != WUSH_OK) return WUSH_ERR_CUDA;
-  const int64_t grid = int64_t(ctas) * sms < a.rows ? int64_t(ctas) * sms : a.rows;
+  const int64_t most = int64_t(ctas) * sms / 4 * 4, grid = most < a.rows ? most : a.rows;
   return launch_pdl(kern, static_cast<unsigned>(grid), G, smem, st, a, q);
 }
 
 // Threads of a row: 256 with up to 32 elements each; fewer for narrow rows, more for wide
 // ones.
-template <bool VEC>
+template <int MODE>
 int launch_width(const Args& a, int sms, cudaStream_t st) {
-  if (a.d <= 1024) return launch_ring<VEC, 1, 128>(a, sms, st);
-  if (a.d <= 2048) return launch_ring<VEC, 1, 256>(a, sms, st);
-  if (a.d <= 4096) return launch_ring<VEC, 2, 256>(a, sms, st);
-  if (a.d <= 6144) return launch_ring<VEC, 3, 256>(a, sms, st);
-  if (a.d <= 8192) return launch_ring<VEC, 4, 256>(a, sms, st);
-  if (a.d <= 12288) return launch_ring<VEC, 3, 512>(a, sms, st);
-  if (a.d <= 16384) return launch_ring<VEC, 4, 512>(a, sms, st);
-  return launch_ring<VEC, 4, 1024>(a, sms, st);
+  const int d = a.d + (MODE == kShifted ? 3 : 0);
+  if (d <= 1024) return launch_ring<MODE, 1, 128>(a, sms, st);
+  if (d <= 2048) return launch_ring<MODE, 1, 256>(a, sms, st);
+  if (d <= 4096) return launch_ring<MODE, 2, 256>(a, sms, st);
+  if (d <= 6144) return launch_ring<MODE, 3, 256>(a, sms, st);
+  if (d <= 8192) return launch_ring<MODE, 4, 256>(a, sms, st);
+  if (d <= 12288) return launch_ring<MODE, 3, 512>(a, sms, st);
+  if (d <= 16384) return launch_ring<MODE, 4, 512>(a, sms, st);
+  return launch_ring<MODE, 4, 1024>(a, sms, st);
+}
+
+// Whether every matrix's rows begin equally far behind a quad's boundary (Columns); the
+// first row's distance and the step from row to row.
+bool shifted(Args* a) {
+  const struct { const void* p; int dt; int64_t stride; } m[5] = {
+      {a->y, a->y_dt, a->y_stride}, {a->r, a->r_dt, a->r_stride},
+      {a->gate_stride ? a->gate : nullptr, a->gate_dt, a->gate_stride},
+      {a->r_out, a->r_dt, a->r_out_stride}, {a->h, a->h_dt, a->h_stride}};
+  int phase = -1, step = 0;
+  for (const auto& t : m) {
+    if (!t.p) continue;
+    const int at = static_cast<int>(reinterpret_cast<uintptr_t>(t.p) / dtype_bytes(t.dt) & 3);
+    const int by = static_cast<int>(t.stride & 3);
+    if (phase >= 0 && (at != phase || by != step)) return false;
+    phase = at;
+    step = by;
+  }
+  a->phase = phase;
+  a->phase_step = step;
+  return a->d + 3 <= kMaxWidth;
 }
 
 int round_up(int n, int m) { return (n + m - 1) / m * m; }
@@ -529,10 +571,11 @@ int run(Args& a, bool vec, cudaStream_t st) {
     a.row_threads = threads;
     const int block = threads < kMinThreads ? kMinThreads : threads;
     const int64_t per = block / threads, grid = (a.rows + per - 1) / per;
-    return vec ? launch_pdl(norm_few_kernel<true>, static_cast<unsigned>(grid), block, 0, st, a)
-               : launch_pdl(norm_few_kernel<false>, static_cast<unsigned>(grid), block, 0, st, a);
+    return vec ? launch_pdl(norm_few_kernel<kAligned>, static_cast<unsigned>(grid), block, 0, st, a)
+               : launch_pdl(norm_few_kernel<kScalar>, static_cast<unsigned>(grid), block, 0, st, a);
   }
-  return vec ? launch_width<true>(a, sms, st) : launch_width<false>(a, sms, st);
+  if (vec) return launch_width<kAligned>(a, sms, st);
+  return shifted(&a) ? launch_width<kShifted>(a, sms, st) : launch_width<kScalar>(a, sms, st);
 }
 
 }  // namespace

@@ -117,51 +117,74 @@ __device__ __forceinline__ float load1(const void* p, int64_t i) {
   return __half2float(static_cast<const __half*>(p)[i]);
 }
 
-// Eight elements of a row as one thread of G holds them.  VEC: two quads, 4 G apart, so
-// that a warp's accesses are contiguous in every type (16 bytes a lane in fp32, 8 in
-// 16 bits); columns at or beyond d (a multiple of 4) read as zero.  Otherwise eight
-// single elements, G apart.
-template <bool VEC>
-__device__ __forceinline__ int group_column(int j, int e, int g, int tid) {
-  return VEC ? ((2 * j + (e >> 2)) * g + tid) * 4 + (e & 3) : (j * 8 + e) * g + tid;
-}
+// How a row's elements go to the ``g`` threads that hold it, eight to a group.
+//   kAligned:  every row of every matrix begins on a 16-byte boundary and d is a multiple of
+//              8: two quads of elements a group, 4 g apart, so that a warp's accesses are
+//              contiguous in every type (16 bytes a lane in fp32, 8 in 16 bits);
+//   kShifted:  the rows begin at any element, but the same number (``shift``) of elements
+//              behind a quad's boundary in every matrix, as in contiguous matrices of an odd
+//              width: the same quads, begun ``shift`` columns before the row.  Quads that the
+//              row fills in part are accessed by the element;
+//   kScalar:   anything else: eight single elements, g apart.
+enum : int { kScalar = 0, kShifted = 1, kAligned = 2 };
 
-template <int DT, bool VEC>
-__device__ __forceinline__ void load_group(const void* row, int j, int g, int tid, int d, float (&v)[8]) {
+template <int MODE>
+struct Columns {
+  int g, tid, d, shift;
+  __device__ __forceinline__ int at(int j, int e) const {
+    return MODE == kScalar ? (j * 8 + e) * g + tid
+                           : ((2 * j + (e >> 2)) * g + tid) * 4 + (e & 3) - (MODE == kShifted ? shift : 0);
+  }
+  __device__ __forceinline__ bool has(int c) const { return (MODE != kShifted || c >= 0) && c < d; }
+  __device__ __forceinline__ bool whole(int c) const {   // the quad from column c (kAligned: or none of it)
+    return MODE == kShifted ? c >= 0 && c + 3 < d : c < d;
+  }
+};
+
+// A group of a row; columns that the row does not have read as zero.  LOOSE: the row is a
+// vector whose quads need not be aligned with the matrices'.
+template <int DT, int MODE, bool LOOSE = false>
+__device__ __forceinline__ void load_group(const void* row, int j, const Columns<MODE>& q, float (&v)[8]) {
   using T = typename std::conditional<DT == WUSH_FP32, float, uint16_t>::type;
   const T* p = static_cast<const T*>(row);
   auto convert = [](uint32_t u) {
     return DT == WUSH_BF16 ? bf16_lo(u) : __half2float(__ushort_as_half(static_cast<unsigned short>(u)));
   };
-  if (VEC) {
+  auto one = [&](int e) {
+    const int c = q.at(j, e);
+    if (DT == WUSH_FP32) v[e] = q.has(c) ? static_cast<const float*>(row)[c] : 0.0f;
+    else v[e] = convert(q.has(c) ? static_cast<const uint16_t*>(row)[c] : 0u);
+  };
+  if (MODE == kScalar || (MODE == kShifted && LOOSE)) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = group_column<true>(j, 4 * h, g, tid);
+    for (int e = 0; e < 8; ++e) one(e);
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = q.at(j, 4 * h);
+    if (q.whole(c)) {
       if (DT == WUSH_FP32) {
-        float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (c < d) q = *reinterpret_cast<const float4*>(p + c);
-        v[4 * h] = q.x; v[4 * h + 1] = q.y; v[4 * h + 2] = q.z; v[4 * h + 3] = q.w;
+        const float4 u = *reinterpret_cast<const float4*>(p + c);
+        v[4 * h] = u.x; v[4 * h + 1] = u.y; v[4 * h + 2] = u.z; v[4 * h + 3] = u.w;
       } else {
-        uint2 q = make_uint2(0u, 0u);
-        if (c < d) q = *reinterpret_cast<const uint2*>(p + c);
-        v[4 * h] = convert(q.x & 0xffffu); v[4 * h + 1] = convert(q.x >> 16);
-        v[4 * h + 2] = convert(q.y & 0xffffu); v[4 * h + 3] = convert(q.y >> 16);
+        const uint2 u = *reinterpret_cast<const uint2*>(p + c);
+        v[4 * h] = convert(u.x & 0xffffu); v[4 * h + 1] = convert(u.x >> 16);
+        v[4 * h + 2] = convert(u.y & 0xffffu); v[4 * h + 3] = convert(u.y >> 16);
       }
-    }
-  } else {
+    } else if (MODE == kShifted) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = group_column<false>(j, e, g, tid);
-      if (DT == WUSH_FP32) v[e] = c < d ? static_cast<const float*>(row)[c] : 0.0f;
-      else v[e] = convert(c < d ? static_cast<const uint16_t*>(row)[c] : 0u);
+      for (int e = 0; e < 4; ++e) one(4 * h + e);
+    } else {
+      v[4 * h] = v[4 * h + 1] = v[4 * h + 2] = v[4 * h + 3] = 0.0f;
     }
   }
 }
 
 // Each element is rounded once, to nearest even (fp16 beyond its range becomes an
 // infinity).
-template <int DT, bool VEC>
-__device__ __forceinline__ void store_group(void* row, int j, int g, int tid, int d, const float (&v)[8]) {
+template <int DT, int MODE>
+__device__ __forceinline__ void store_group(void* row, int j, const Columns<MODE>& q, const float (&v)[8]) {
   uint32_t u[4];
   if (DT != WUSH_FP32) {
 #pragma unroll
@@ -175,24 +198,29 @@ __device__ __forceinline__ void store_group(void* row, int j, int g, int tid, in
       }
     }
   }
-  if (VEC) {
+  auto one = [&](int e) {
+    const int c = q.at(j, e);
+    if (!q.has(c)) return;
+    if (DT == WUSH_FP32) static_cast<float*>(row)[c] = v[e];
+    else static_cast<uint16_t*>(row)[c] = static_cast<uint16_t>(e & 1 ? u[e / 2] >> 16 : u[e / 2]);
+  };
+  if (MODE == kScalar) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = group_column<true>(j, 4 * h, g, tid);
-      if (c >= d) continue;
+    for (int e = 0; e < 8; ++e) one(e);
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = q.at(j, 4 * h);
+    if (q.whole(c)) {
       if (DT == WUSH_FP32)
         *reinterpret_cast<float4*>(static_cast<float*>(row) + c) =
             make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
       else
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(row) + c) = make_uint2(u[2 * h], u[2 * h + 1]);
-    }
-  } else {
+    } else if (MODE == kShifted) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = group_column<false>(j, e, g, tid);
-      if (c >= d) continue;
-      if (DT == WUSH_FP32) static_cast<float*>(row)[c] = v[e];
-      else static_cast<uint16_t*>(row)[c] = static_cast<uint16_t>(e & 1 ? u[e / 2] >> 16 : u[e / 2]);
+      for (int e = 0; e < 4; ++e) one(4 * h + e);
     }
   }
 }

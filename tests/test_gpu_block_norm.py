@@ -86,7 +86,8 @@ def check(lib, rows, d, y="fp32", r="bf16", h="bf16", w="bf16", post="rms", pre=
 @pytest.mark.parametrize("rows, d", [(1, 1), (1, 8), (3, 5), (2, 256), (9, 100), (5, 1000), (1, 4096), (299, 4096),
                                      (301, 1024), (700, 136), (2, 12288), (3, 8200), (1, 32768), (2, 32767),
                                      (310, 4100), (4, 16392), (1531, 257), (900, 40), (1000, 2048), (400, 8192), (333, 12288), (310, 20000),
-                                     (320, 32768), (305, 32767), (600, 6145)])
+                                     (320, 32768), (305, 32767), (600, 6145), (597, 4094), (400, 8191), (311, 12289), (303, 16385), (301, 24571),
+                                     (300, 2), (3000, 3), (2048, 1023)])
 @pytest.mark.parametrize("kind", ["rms", "layer"])
 def test_sizes(lib, rows, d, kind):
     check(lib, rows, d, post=kind, pre=kind, bias=kind == "layer", gate="element", act="silu")
@@ -141,6 +142,22 @@ def test_strided_rows_and_their_surroundings(lib, d, wide, at):
             edge = big.clone()
             edge[1:-1, at:at + d] = 7.0
             assert bool((edge == 7.0).all())
+
+
+@pytest.mark.parametrize("rows", [7, 700])
+@pytest.mark.parametrize("d", [256, 257, 1030])
+def test_tensors_whose_rows_begin_apart(lib, rows, d):
+    # row strides and first columns that agree in nothing
+    at = {"y": 1, "r": 2, "r_out": 3, "h": 5, "gate": 0}
+
+    def make(t, name):
+        big = torch.full((t.shape[0] + 1, d + 8 + at[name]), 7.0, dtype=t.dtype, device="cuda")
+        view = big[:-1, at[name]:at[name] + d]
+        view.copy_(t)
+        return view
+
+    for kw in (dict(), dict(post="layer", pre="layer", bias=True, gate="element", act="silu"), dict(gate="channel")):
+        check(lib, rows, d, make=make, **kw)
 
 
 def test_outputs_side_by_side_in_one_buffer(lib):
