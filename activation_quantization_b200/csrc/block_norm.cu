@@ -11,10 +11,14 @@
 // reduction), and no element is read from memory twice.
 //
 // Two kernels share that arithmetic:
-//  * few rows: one CTA a row, loads straight to registers (latency counts);
+//  * few rows, or narrow ones: one CTA a row (narrow rows share one), loads straight to
+//    registers (latency counts);
 //  * many rows: persistent CTAs, each with a ring of whole rows in shared memory that
 //    bulk copies fill ahead of it, so that the bytes in flight do not depend on how
-//    many threads wait.
+//    many threads wait.  4096 rows x 4096, fp32 y, bf16 stream and h: 29.0 us, 5.79 TB/s;
+//    8192 x 5120 bf16, the norm alone: 30.3 us, 5.54 TB/s; 2048 x 12288 fp32 with layer
+//    norms and a gate per element: 92 us, 4.93 TB/s (its four vectors do not fit beside
+//    the rows and are read from L2 for each row).
 #include "rowops.cuh"
 #include "sm100.cuh"
 
@@ -126,7 +130,11 @@ __device__ __forceinline__ void apply_norm(const Args& a, const NormArgs& n, con
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[j][e] = q.has(q.at(j, e)) ? v[j][e] - mean : 0.0f;
+      for (int e = 0; e < 8; ++e) {
+        const int c = MODE == kScalar ? q.at(j, e) : q.at(j, e & 4);     // (a quad's first column speaks for it)
+        v[j][e] = c < q.d ? v[j][e] - mean : 0.0f;
+      }
+    mask_edges<MODE, NV>(q, v);
   }
   float2 sq = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -140,7 +148,7 @@ __device__ __forceinline__ void apply_norm(const Args& a, const NormArgs& n, con
       scale8(v[j], f);
       mul8(v[j], x);
     }
-  } else if (n.w) {
+  } else if (MODE != kShifted && n.w) {
     with_dtype(n.dt, [&](auto dt) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -163,7 +171,7 @@ __device__ __forceinline__ void apply_norm(const Args& a, const NormArgs& n, con
       load_group<WUSH_FP32, MODE>(vec.b, j, q, x);
       add8(v[j], x);
     }
-  } else if (n.b) {
+  } else if (MODE != kShifted && n.b) {
     with_dtype(n.dt, [&](auto dt) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -181,6 +189,7 @@ __device__ __forceinline__ void load_row(const void* row, int dt, const Columns<
 #pragma unroll
     for (int j = 0; j < NV; ++j) load_group<t.value, MODE>(row, j, q, v[j]);
   });
+  mask_edges<MODE, NV>(q, v);
 }
 
 template <int MODE, int NV>
@@ -191,18 +200,16 @@ __device__ __forceinline__ void store_row(void* row, int dt, const Columns<MODE>
   });
 }
 
-// v = residual_scale * r + branch_scale * v * act(gate).  ``loose``: the gate is a vector in
-// the caller's memory.
+// v = residual_scale * r + branch_scale * v * act(gate).
 template <int MODE, int NV>
-__device__ __forceinline__ void gate_and_add(const Args& a, const void* gate, int gate_dt, bool loose, const void* r,
+__device__ __forceinline__ void gate_and_add(const Args& a, const void* gate, int gate_dt, const void* r,
                                              float (&v)[NV][8], const Columns<MODE>& q) {
   if (gate)
     with_dtype(gate_dt, [&](auto t) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float x[8];
-        if (MODE == kShifted && loose) load_group<t.value, MODE, true>(gate, j, q, x);
-        else load_group<t.value, MODE>(gate, j, q, x);
+        load_group<t.value, MODE>(gate, j, q, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[j][e] *= activate(x[e], a.act);
       }
@@ -220,10 +227,11 @@ __device__ __forceinline__ void gate_and_add(const Args& a, const void* gate, in
 #pragma unroll
     for (int j = 0; j < NV; ++j) scale8(v[j], a.branch_scale);
   }
+  mask_edges<MODE, NV>(q, v);
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: one CTA a row (narrow rows share one).
+// Few or narrow rows: one CTA a row, narrow rows sharing one.
 // ---------------------------------------------------------------------------
 template <int MODE>
 __global__ void __launch_bounds__(1024) norm_few_kernel(const __grid_constant__ Args a) {
@@ -231,7 +239,7 @@ __global__ void __launch_bounds__(1024) norm_few_kernel(const __grid_constant__ 
   const int g = a.row_threads, sub = threadIdx.x / g, tid = threadIdx.x - sub * g, warp0 = sub * (g >> 5);
   const int64_t row = int64_t(blockIdx.x) * (blockDim.x / g) + sub;
   const bool live = row < a.rows;                          // the others only take part in the barriers
-  const Columns<MODE> q = {g, tid, live ? a.d : 0, 0};
+  const Columns<MODE> q = {g, tid, live ? a.d : 0, 0, false};
   float v[1][8];
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
@@ -239,7 +247,7 @@ __global__ void __launch_bounds__(1024) norm_few_kernel(const __grid_constant__ 
   if (a.y) {
     load_row<MODE, 1>(row_of(a.y, a.y_dt, row * a.y_stride), a.y_dt, q, v);
     apply_norm<MODE, 1>(a, a.post, Vectors{}, v, red, q, warp0);
-    gate_and_add<MODE, 1>(a, a.gate ? row_of(a.gate, a.gate_dt, row * a.gate_stride) : nullptr, a.gate_dt, false, r, v, q);
+    gate_and_add<MODE, 1>(a, a.gate ? row_of(a.gate, a.gate_dt, row * a.gate_stride) : nullptr, a.gate_dt, r, v, q);
     if (a.r_out) store_row<MODE, 1>(row_of(a.r_out, a.r_dt, row * a.r_out_stride), a.r_dt, q, v);
   } else {
     load_row<MODE, 1>(r, a.r_dt, q, v);
@@ -271,7 +279,9 @@ __global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __
   constexpr int g = G;                                     // (a constant, so that columns are immediate offsets)
   const int tid = threadIdx.x, d = a.d;
   // (a CTA's rows are gridDim.x apart, a multiple of four, and so all have one shift)
-  const Columns<MODE> cols = {g, tid, d, MODE == kShifted ? (a.phase + (blockIdx.x & 3) * a.phase_step) & 3 : 0};
+  Columns<MODE> cols = {g, tid, d, MODE == kShifted ? (a.phase + static_cast<int>(blockIdx.x & 3) * a.phase_step) & 3 : 0,
+                        false};
+  if (MODE == kShifted) cols.edges = cols.find_edges(NV);
   const bool gate_rows = a.gate && a.gate_stride;
   const int n_rows = static_cast<int>((a.rows - 1 - blockIdx.x) / gridDim.x) + 1;   // (at most one CTA a row)
 
@@ -286,22 +296,7 @@ __global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __
   for (int i = tid; i < 2 * 4 * 32; i += g) (&red[0][0][0])[i] = 0.0f;
   sm100::pdl_wait();                                       // nothing global is touched before this
   sm100::pdl_launch_dependents();
-  // the vectors that every row uses, as fp32 and shifted like the rows
-  auto stage = [&](const void* p, int dt, int at, float offset) -> const float* {
-    if (!p || at < 0) return nullptr;
-    float* out = reinterpret_cast<float*>(smem + at) + cols.shift;
-    with_dtype(dt, [&](auto t) __attribute__((always_inline)) {
-      for (int i = tid; i < d; i += g) out[i] = load1<t.value>(p, i) + offset;
-    });
-    return out;
-  };
-  const Vectors post = {q.kept, stage(a.post.w, a.post.dt, q.vec[0], a.post.offset),
-                        stage(a.post.b, a.post.dt, q.vec[1], 0.0f)};
-  const Vectors pre = {q.kept, stage(a.pre.w, a.pre.dt, q.vec[2], a.pre.offset),
-                       stage(a.pre.b, a.pre.dt, q.vec[3], 0.0f)};
-  const float* gate_vec = gate_rows ? nullptr : stage(a.gate, a.gate_dt, q.vec[4], 0.0f);
-  __syncthreads();
-
+  __syncthreads();                                         // the barriers are set up
   // One row of one tensor into its stage, by a bulk copy (thread 0) of the 16-byte units that
   // it touches: ``units`` gives their first byte and their number of bytes.  What a unit holds
   // beside the row is never used.  Units that reach beyond the matrix (its first row's first,
@@ -391,6 +386,49 @@ __global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __
     fill_y(i, i);
     fill_rest(i, i);
   }
+  // Meanwhile the vectors that every row uses, as fp32 and shifted like the rows; all of a
+  // thread's elements of all vectors are asked for before any is stored.
+  Vectors post = {q.kept, nullptr, nullptr}, pre = post;
+  const float* gate_vec = nullptr;
+  if (q.kept) {
+    const void* src[5] = {a.post.w, a.post.b, a.pre.w, a.pre.b, gate_rows ? nullptr : a.gate};
+    const int dts[5] = {a.post.dt, a.post.dt, a.pre.dt, a.pre.dt, a.gate_dt};
+    const float offset[5] = {a.post.offset, 0.0f, a.pre.offset, 0.0f, 0.0f};
+    float* dst[5];
+#pragma unroll
+    for (int n = 0; n < 5; ++n) dst[n] = src[n] ? reinterpret_cast<float*>(smem + q.vec[n]) + cols.shift : nullptr;
+    const bool alike = (!src[2] && !src[3] || !src[0] && !src[1] || dts[0] == dts[2]) && (!src[4] || dts[4] == dts[2]);
+#pragma unroll 1
+    for (int j = 0; j < NV; ++j) {
+      float x[5][8];
+      if (alike) {
+        with_dtype(src[2] || src[3] || src[4] ? src[4] ? dts[4] : dts[2] : dts[0], [&](auto t) __attribute__((always_inline)) {
+#pragma unroll
+          for (int n = 0; n < 5; ++n)
+            if (src[n]) load_group<t.value, MODE, true>(src[n], j, cols, x[n]);
+        });
+      } else {
+#pragma unroll
+        for (int n = 0; n < 5; ++n)
+          if (src[n])
+            with_dtype(dts[n], [&](auto t) __attribute__((always_inline)) {
+              load_group<t.value, MODE, true>(src[n], j, cols, x[n]);
+            });
+      }
+#pragma unroll
+      for (int n = 0; n < 5; ++n)
+        if (src[n])
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int c = cols.at(j, e);
+            if (cols.has(c)) dst[n][c] = x[n][e] + offset[n];
+          }
+    }
+    post.w = dst[0]; post.b = dst[1];
+    pre.w = dst[2]; pre.b = dst[3];
+    gate_vec = dst[4];
+    __syncthreads();
+  }
   int s = 0;
   uint32_t parity = 0;
   for (int i = 0; i < n_rows; ++i) {
@@ -415,7 +453,7 @@ __global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __
       if (gate_ring) gate = smem + q.gate + s * q.gate_step + phase(a.gate, a.gate_dt, a.gate_stride);
       else if (gate_vec) gate = gate_vec, gate_dt = WUSH_FP32;
       else if (a.gate) gate = row_of(a.gate, a.gate_dt, row * a.gate_stride);
-      gate_and_add<MODE, NV>(a, gate, gate_dt, !gate_rows && !gate_vec,
+      gate_and_add<MODE, NV>(a, gate, gate_dt,
                              r_ring ? r_stage : a.r ? row_of(a.r, a.r_dt, row * a.r_stride) : nullptr, v, cols);
       if (a.r_out) store_row<MODE, NV>(row_of(a.r_out, a.r_dt, row * a.r_out_stride), a.r_dt, cols, v);
     } else {
@@ -476,9 +514,10 @@ constexpr int kInFlight = 96 * 1024;                       // bytes of rows that
 // An SM needs some 50 KB in flight to fill its share of the memory's bandwidth; with as
 // many CTAs as the registers allow, one stage each gives that for rows of 24 KB (a stage
 // is refilled while its row is still being worked on in registers) and narrower rows take
-// up to four.  Measured at 4096 rows x 4096 (fp32 y, bf16 stream): four CTAs of 256
-// threads with one stage 30.7 us, two with two stages 34.4 us, eight of 128 threads 32.5 us;
-// at 8192 x 5120 bf16: 32.1 us with two stages, 36.6 us with one.
+// up to four.  Measured (before the programmatic launch took another 2 us off) at 4096 rows
+// x 4096, fp32 y, bf16 stream: four CTAs of 256 threads with one stage 30.7 us, two with two
+// stages 34.4 us, eight of 128 threads 32.5 us; at 8192 x 5120 bf16, three CTAs: 31.3 us with
+// three stages, 33.1 us with two.
 int plan(const Args& a, bool aligned, int ctas, Ring* q) {
   const int budget = kSmemPerSm / ctas - kCtaOverhead;
   auto up = [](int64_t n) { return static_cast<int>((n + 15) / 16 * 16); };
@@ -511,7 +550,13 @@ int plan(const Args& a, bool aligned, int ctas, Ring* q) {
 template <int MODE, int NV, int G>
 int launch_ring(const Args& a, int sms, cudaStream_t st) {
   Ring q = {};
-  const int ctas = ring_ctas(NV, G), smem = plan(a, MODE == kAligned, ctas, &q);
+  int ctas = ring_ctas(NV, G), smem = plan(a, MODE == kAligned, ctas, &q);
+  if (MODE == kShifted) {                                  // all in shared memory, with fewer CTAs if need be
+    const bool gate_rows = a.gate && a.gate_stride;
+    while (ctas > 1 && !(q.kept && (!a.r || q.r >= 0) && (!gate_rows || q.gate >= 0)))
+      smem = plan(a, false, --ctas, &q);
+    if (!(q.kept && (!a.r || q.r >= 0) && (!gate_rows || q.gate >= 0))) return WUSH_ERR_UNSUPPORTED;
+  }
   auto kern = norm_ring_kernel<MODE, NV, G>;
   static std::atomic<uint64_t> done{0};
   if (set_smem_once(kern, kSmemPerSm, done) != WUSH_OK) return WUSH_ERR_CUDA;
@@ -519,13 +564,10 @@ int launch_ring(const Args& a, int sms, cudaStream_t st) {
   return launch_pdl(kern, static_cast<unsigned>(grid), G, smem, st, a, q);
 }
 
-// Threads of a row: 256 with up to 32 elements each; fewer for narrow rows, more for wide
-// ones.
+// Threads of a row: 256 with up to 32 elements each, more for wide rows.
 template <int MODE>
 int launch_width(const Args& a, int sms, cudaStream_t st) {
   const int d = a.d + (MODE == kShifted ? 3 : 0);
-  if (d <= 1024) return launch_ring<MODE, 1, 128>(a, sms, st);
-  if (d <= 2048) return launch_ring<MODE, 1, 256>(a, sms, st);
   if (d <= 4096) return launch_ring<MODE, 2, 256>(a, sms, st);
   if (d <= 6144) return launch_ring<MODE, 3, 256>(a, sms, st);
   if (d <= 8192) return launch_ring<MODE, 4, 256>(a, sms, st);
@@ -564,8 +606,10 @@ int run(Args& a, bool vec, cudaStream_t st) {
     return WUSH_ERR_CUDA;
   const int groups = (a.d + 7) / 8;
   a.inv_d = 1.0f / static_cast<float>(a.d);
-  // Few rows: the ring's set-up would cost more than it hides.
-  if (a.rows <= 2 * sms && groups <= 1024) {
+  // Few rows, or narrow ones: the ring's set-up would cost more than it hides.  Measured: 7696
+  // rows of 174, 16 bits: 4.9 us and 29 us by the ring; 5536 of 1216, fp32 y, layer norm, gate:
+  // 24.9 and 35.5 us; 4096 of 4096, fp32 y: 38.7 and 29.0 us.
+  if ((a.rows <= 2 * sms && groups <= 1024) || groups <= 256) {
     int threads = round_up(groups, 32);
     if (threads < kMinThreads) threads = threads <= 32 ? 32 : threads <= 64 ? 64 : kMinThreads;
     a.row_threads = threads;
@@ -575,7 +619,11 @@ int run(Args& a, bool vec, cudaStream_t st) {
                : launch_pdl(norm_few_kernel<kScalar>, static_cast<unsigned>(grid), block, 0, st, a);
   }
   if (vec) return launch_width<kAligned>(a, sms, st);
-  return shifted(&a) ? launch_width<kShifted>(a, sms, st) : launch_width<kScalar>(a, sms, st);
+  if (shifted(&a)) {
+    const int rc = launch_width<kShifted>(a, sms, st);
+    if (rc != WUSH_ERR_UNSUPPORTED) return rc;
+  }
+  return launch_width<kScalar>(a, sms, st);
 }
 
 }  // namespace

@@ -109,14 +109,6 @@ __device__ __forceinline__ float2 squares8(const float (&v)[8], float2 s) {
   return s;
 }
 
-// One element.
-template <int DT>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-  if (DT == WUSH_FP32) return static_cast<const float*>(p)[i];
-  if (DT == WUSH_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  return __half2float(static_cast<const __half*>(p)[i]);
-}
-
 // How a row's elements go to the ``g`` threads that hold it, eight to a group.
 //   kAligned:  every row of every matrix begins on a 16-byte boundary and d is a multiple of
 //              8: two quads of elements a group, 4 g apart, so that a warp's accesses are
@@ -131,18 +123,38 @@ enum : int { kScalar = 0, kShifted = 1, kAligned = 2 };
 template <int MODE>
 struct Columns {
   int g, tid, d, shift;
+  bool edges;                                              // kShifted: the warp has quads that the row fills in part
   __device__ __forceinline__ int at(int j, int e) const {
     return MODE == kScalar ? (j * 8 + e) * g + tid
                            : ((2 * j + (e >> 2)) * g + tid) * 4 + (e & 3) - (MODE == kShifted ? shift : 0);
   }
   __device__ __forceinline__ bool has(int c) const { return (MODE != kShifted || c >= 0) && c < d; }
-  __device__ __forceinline__ bool whole(int c) const {   // the quad from column c (kAligned: or none of it)
-    return MODE == kShifted ? c >= 0 && c + 3 < d : c < d;
+  // The same for all threads of a warp, for NV groups a thread.
+  __device__ __forceinline__ bool find_edges(int nv) const {
+    bool part = false;
+    for (int j = 0; j < nv; ++j)
+      for (int h = 0; h < 2; ++h) {
+        const int c = at(j, 4 * h);
+        part = part || (c < d && (c < 0 || c + 3 >= d));
+      }
+    return __any_sync(0xffffffffu, part);
   }
 };
 
-// A group of a row; columns that the row does not have read as zero.  LOOSE: the row is a
-// vector whose quads need not be aligned with the matrices'.
+// Zeroes the elements of quads that the row does not have.
+template <int MODE, int NV>
+__device__ __forceinline__ void mask_edges(const Columns<MODE>& q, float (&v)[NV][8]) {
+  if (MODE != kShifted || !q.edges) return;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[j][e] = q.has(q.at(j, e)) ? v[j][e] : 0.0f;
+}
+
+// A group of a row; columns that the row does not have read as zero.  In kShifted the row
+// lies in shared memory, where whole quads can be read at its ends, and their elements
+// outside the row are whatever lies there (mask_edges).  LOOSE: the row is a
+// vector in global memory whose quads need not be aligned with the matrices'.
 template <int DT, int MODE, bool LOOSE = false>
 __device__ __forceinline__ void load_group(const void* row, int j, const Columns<MODE>& q, float (&v)[8]) {
   using T = typename std::conditional<DT == WUSH_FP32, float, uint16_t>::type;
@@ -150,33 +162,27 @@ __device__ __forceinline__ void load_group(const void* row, int j, const Columns
   auto convert = [](uint32_t u) {
     return DT == WUSH_BF16 ? bf16_lo(u) : __half2float(__ushort_as_half(static_cast<unsigned short>(u)));
   };
-  auto one = [&](int e) {
-    const int c = q.at(j, e);
-    if (DT == WUSH_FP32) v[e] = q.has(c) ? static_cast<const float*>(row)[c] : 0.0f;
-    else v[e] = convert(q.has(c) ? static_cast<const uint16_t*>(row)[c] : 0u);
-  };
-  if (MODE == kScalar || (MODE == kShifted && LOOSE)) {
+  if constexpr (MODE == kScalar || (MODE == kShifted && LOOSE)) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) one(e);
-    return;
-  }
+    for (int e = 0; e < 8; ++e) {
+      const int c = q.at(j, e);
+      if (DT == WUSH_FP32) v[e] = q.has(c) ? static_cast<const float*>(row)[c] : 0.0f;
+      else v[e] = convert(q.has(c) ? static_cast<const uint16_t*>(row)[c] : 0u);
+    }
+  } else {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int c = q.at(j, 4 * h);
-    if (q.whole(c)) {
+    for (int h = 0; h < 2; ++h) {
+      const int c = q.at(j, 4 * h);
       if (DT == WUSH_FP32) {
-        const float4 u = *reinterpret_cast<const float4*>(p + c);
+        float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (c < q.d) u = *reinterpret_cast<const float4*>(p + c);
         v[4 * h] = u.x; v[4 * h + 1] = u.y; v[4 * h + 2] = u.z; v[4 * h + 3] = u.w;
       } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(p + c);
+        uint2 u = make_uint2(0u, 0u);
+        if (c < q.d) u = *reinterpret_cast<const uint2*>(p + c);
         v[4 * h] = convert(u.x & 0xffffu); v[4 * h + 1] = convert(u.x >> 16);
         v[4 * h + 2] = convert(u.y & 0xffffu); v[4 * h + 3] = convert(u.y >> 16);
       }
-    } else if (MODE == kShifted) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) one(4 * h + e);
-    } else {
-      v[4 * h] = v[4 * h + 1] = v[4 * h + 2] = v[4 * h + 3] = 0.0f;
     }
   }
 }
@@ -204,23 +210,19 @@ __device__ __forceinline__ void store_group(void* row, int j, const Columns<MODE
     if (DT == WUSH_FP32) static_cast<float*>(row)[c] = v[e];
     else static_cast<uint16_t*>(row)[c] = static_cast<uint16_t>(e & 1 ? u[e / 2] >> 16 : u[e / 2]);
   };
-  if (MODE == kScalar) {
+  if (MODE == kScalar || (MODE == kShifted && q.edges)) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) one(e);
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int c = q.at(j, 4 * h);
-    if (q.whole(c)) {
+    for (int h = 0; h < 2; ++h) {
+      const int c = q.at(j, 4 * h);
+      if (c >= q.d) continue;
       if (DT == WUSH_FP32)
         *reinterpret_cast<float4*>(static_cast<float*>(row) + c) =
             make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
       else
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(row) + c) = make_uint2(u[2 * h], u[2 * h + 1]);
-    } else if (MODE == kShifted) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) one(4 * h + e);
     }
   }
 }
