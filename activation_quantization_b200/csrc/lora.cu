@@ -46,6 +46,7 @@ __device__ __forceinline__ void report_timeout() {
 
 constexpr int kMaxRank = 256;
 constexpr int64_t kMaxAdapters = 1 << 20, kMaxWidth = 1 << 24, kMaxTokens = 1 << 24;
+constexpr int64_t kMaxStride = int64_t(1) << 38;           // of a tensor map's rows
 
 struct LoraArgs {
   const void* x;
@@ -240,8 +241,16 @@ __global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const __grid_cons
   const int my_tok = s_tok[row];
   const E* x = my_tok >= 0 ? static_cast<const E*>(p.x) + my_tok * p.x_stride : nullptr;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  float acc[MB][4] = {};
+  float acc[MB][4] = {}, sum[MB][4] = {};
+  int steps = 0;
   for (int kb = cta * kFewWarps + warp; kb < p.d_in / 32; kb += kCluster * kFewWarps) {
+    if (steps++ == 16) {                                   // (chains of 32 MMAs: see kChain)
+      steps = 1;
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[m][j] += acc[m][j], acc[m][j] = 0.0f;
+    }
     const int col = kb * 32 + c * 8;
     const uint4 xv = x ? *reinterpret_cast<const uint4*>(x + col) : zero;
     uint4 lo[MB], hi[MB];
@@ -260,8 +269,8 @@ __global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const __grid_cons
 #pragma unroll
   for (int m = 0; m < MB; ++m) {
     float* o = part + (warp * kR + m * 16 + row) * 8 + c * 2;
-    *reinterpret_cast<float2*>(o) = make_float2(acc[m][0], acc[m][1]);
-    *reinterpret_cast<float2*>(o + 64) = make_float2(acc[m][2], acc[m][3]);
+    *reinterpret_cast<float2*>(o) = make_float2(sum[m][0] + acc[m][0], sum[m][1] + acc[m][1]);
+    *reinterpret_cast<float2*>(o + 64) = make_float2(sum[m][2] + acc[m][2], sum[m][3] + acc[m][3]);
   }
   __syncthreads();
   const int used = (k + 15) / 16 * 16 * 8;                 // of s, [rank][token]
@@ -403,7 +412,7 @@ int launch_few(const LoraArgs& p, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 constexpr int kTile = 64, kCols = 64;
 constexpr int kMaxSmem = 226 * 1024;                      // dynamic; the rest for a kernel's own
-constexpr int kPlanThreads = 1024, kPlanAdapters = 12288;  // adapters whose counts fit the plan's shared memory
+constexpr int kPlanThreads = 1024, kPlanAdapters = 57344;  // adapters whose counts fit the plan's shared memory
 constexpr int kShrinkThreads = 192;
 
 struct Counts {
@@ -1242,9 +1251,10 @@ int launch_many(const LoraArgs& p, const Work& w, cudaStream_t st) {
 // adapter, 576 x 5296, rank 96: 37.6 and 23.0 us.
 constexpr int kFewTokens = 256;
 
-bool few(int64_t tokens, int64_t n, int64_t d_out) {
-  return tokens <= kFewTokens || n > kPlanAdapters || n * d_out > 0x7fffffff;
-}
+constexpr int64_t kMostFewTokens = 4096;                   // a cluster's look through all tokens stays short
+
+bool large_pool(int64_t n, int64_t d_out) { return n > kPlanAdapters || n * d_out > 0x7fffffff; }
+bool few(int64_t tokens, int64_t n, int64_t d_out) { return tokens <= kFewTokens || large_pool(n, d_out); }
 
 template <typename E>
 int run_lora(const LoraArgs& p, void* workspace, cudaStream_t st) {
@@ -1264,7 +1274,8 @@ bool sizes_ok(int64_t tokens, int64_t d_in, int64_t d_out, int64_t n, int64_t ra
   return tokens >= 0 && d_in > 0 && d_in % 32 == 0 && d_out > 0 && d_out % 8 == 0 && n > 0 && rank > 0 && rank % 8 == 0;
 }
 bool sizes_taken(int64_t tokens, int64_t d_in, int64_t d_out, int64_t n, int64_t rank) {
-  return rank <= kMaxRank && n <= kMaxAdapters && d_in <= kMaxWidth && d_out <= kMaxWidth && tokens <= kMaxTokens;
+  return rank <= kMaxRank && n <= kMaxAdapters && d_in <= kMaxWidth && d_out <= kMaxWidth && tokens <= kMaxTokens &&
+         (tokens <= kMostFewTokens || !large_pool(n, d_out));
 }
 
 }  // namespace
@@ -1296,7 +1307,8 @@ extern "C" int wush_lora_add(const wush_lora_args* args, void* stream) {
   if (q.x_stride < q.d_in || q.x_stride % 8 || q.y_stride < q.d_out || q.y_stride % 4) return WUSH_ERR_INVALID_ARG;
   if (q.y_in && (q.y_in_stride < q.d_out || q.y_in_stride % 4)) return WUSH_ERR_INVALID_ARG;
   const int64_t far = (int64_t(1) << 60) / q.tokens;
-  if (q.x_stride > far || q.y_stride > far || (q.y_in && q.y_in_stride > far)) return WUSH_ERR_UNSUPPORTED;
+  if (q.x_stride > far || q.x_stride > kMaxStride || q.y_stride > far || (q.y_in && q.y_in_stride > far))
+    return WUSH_ERR_UNSUPPORTED;
   const Span out = span(q.y, WUSH_FP32, q.y_stride, q.d_out);
   if (overlap(out, span(q.x, q.dtype, q.x_stride, q.d_in), q.tokens)) return WUSH_ERR_INVALID_ARG;
   if (!(q.y == q.y_in && q.y_stride == q.y_in_stride) &&
@@ -1309,6 +1321,9 @@ extern "C" int wush_lora_add(const wush_lora_args* args, void* stream) {
   if (need) {
     if (!q.workspace || !aligned16(q.workspace)) return WUSH_ERR_INVALID_ARG;
     if (q.workspace_bytes < need) return WUSH_ERR_BUFFER_TOO_SMALL;
+    const Span ws = {static_cast<const char*>(q.workspace), 0, static_cast<int64_t>(need)};
+    for (const Span& t : {out, span(q.x, q.dtype, q.x_stride, q.d_in), span(q.y_in, WUSH_FP32, q.y_in_stride, q.d_out)})
+      if (t.p && ws.p < t.p + (q.tokens - 1) * t.stride + t.width && t.p < ws.p + ws.width) return WUSH_ERR_INVALID_ARG;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return q.dtype == WUSH_FP16 ? run_lora<__half>(p, q.workspace, st) : run_lora<__nv_bfloat16>(p, q.workspace, st);

@@ -522,11 +522,15 @@ int wush_norm(const void* x, int x_dtype, int64_t x_stride, int64_t rows, int64_
  * y_in:     device fp32 [tokens, d_out], row stride a multiple of 4; NULL: zeros.
  * y:        device fp32 [tokens, d_out], row stride a multiple of 4; may be y_in (with
  *           its stride), otherwise it may overlap neither y_in nor x.
- * workspace: device, at least wush_lora_workspace_bytes(...) bytes, 16-byte aligned;
- *           may be NULL where that is 0.  Calls that can overlap in time (two streams,
+ * workspace: device, at least wush_lora_workspace_bytes(...) bytes, 16-byte aligned, apart
+ *           from x, y_in and y; may be NULL where that is 0 (256 tokens or fewer).  Calls that can overlap in time (two streams,
  *           two graphs) need one each.
- * Requirements: tokens >= 0 (0: nothing is launched), d_in % 32 == 0, d_out % 8 == 0,
- * rank % 8 == 0, 8 <= rank <= 256; WUSH_ERR_BUFFER_TOO_SMALL for a small workspace. */
+ *           What it holds before and after a call is of no meaning.
+ * Requirements: 0 <= tokens <= 2^24 (0: nothing is launched), d_in % 32 == 0,
+ * d_out % 8 == 0, both <= 2^24, rank % 8 == 0, 8 <= rank <= 256, n_adapters <= 2^20; with
+ * n_adapters > 57344 or n_adapters * d_out >= 2^31, tokens <= 4096.
+ * WUSH_ERR_BUFFER_TOO_SMALL for a small workspace.  Up to 256 tokens take one launch, more
+ * take three. */
 typedef struct {
   const void* x;
   const int32_t* adapter;

@@ -204,6 +204,35 @@ def test_sizes_of_the_listed_projections(lib):
     check(lib, 300, 12288, 4096, 3, 64)
 
 
+def test_requests_side_by_side_and_apart(lib):
+    # rows of a tile that follow one another are fetched in blocks, the others one by one; pools of
+    # more than 1024 adapters leave the order to chance
+    t = torch.arange(900)
+    for n in (3, 1500):
+        for ad in (t // 300, t // 7 % n, (t * 7919) % n, torch.where(t % 50 < 43, t // 450, t % n)):
+            check(lib, 900, 384, 136, n, 16, adapter=ad)
+    check(lib, 3000, 64, 64, 2, 8, adapter=torch.zeros(3000))    # one adapter with many tiles
+
+
+def test_a_long_row_of_blocks(lib):
+    # enough column blocks that they are drawn from a counter, call after call
+    x, adapter, a, b, base, y, ws, _, st = check(lib, 2500, 64, 4096, 9, 16)
+    for _ in range(3):
+        y2 = torch.empty_like(y)
+        lib.wush_lora_add(x, adapter, a, b, base, y2, ws, None, st)
+        assert torch.equal(y, y2)
+
+
+def test_more_tokens_than_one_look_of_the_plan(lib):
+    check(lib, 20000, 32, 16, 5, 8)
+
+
 def test_a_pool_too_large_to_count_in_shared_memory(lib):
-    assert lib.wush_lora_workspace_bytes(150, 64, 64, 20000, 8) == 0
-    check(lib, 150, 64, 64, 20000, 8, adapter=torch.cat([torch.randperm(20000)[:100], torch.full((50,), 19999)]))
+    assert lib.wush_lora_workspace_bytes(500, 64, 64, 60000, 8) == 0
+    check(lib, 500, 64, 64, 60000, 8, adapter=torch.cat([torch.randperm(60000)[:300], torch.full((200,), 59999)]))
+    check(lib, 400, 32, 64, 57344, 8, adapter=torch.cat([torch.randperm(57344)[:300], torch.full((100,), 57343)]))
+
+
+@pytest.mark.parametrize("tokens", [2, 300])
+def test_a_long_reduction(lib, tokens):
+    check(lib, tokens, 1 << 17, 64, 2, 8)

@@ -32,7 +32,10 @@ def test_shapes_and_types():
     assert call(rank=264) == UNSUPPORTED and call(d_in=1 << 25, xs=1 << 25) == UNSUPPORTED
     assert call(d_out=1 << 25, ys=1 << 25, yis=1 << 25) == UNSUPPORTED and call(tokens=1 << 27) == UNSUPPORTED
     assert call(n=(1 << 20) + 1) == UNSUPPORTED
-    assert call(ys=1 << 58) == UNSUPPORTED
+    assert call(ys=1 << 58) == UNSUPPORTED and call(xs=1 << 39) == UNSUPPORTED
+    # pools too large to sort by
+    assert call(n=60000, tokens=4097) == UNSUPPORTED and call(n=50000, d_out=1 << 16, ys=1 << 16, yis=1 << 16,
+                                                              tokens=4097) == UNSUPPORTED
 
 
 def test_pointers_and_strides():
@@ -55,9 +58,10 @@ def test_overlaps():
 
 def test_workspace():
     need = aq.wush_lora_workspace_bytes(1000, 256, 512, 4, 16)
-    assert need >= 0
-    if need:
-        assert call(wn=need - 1) == TOO_SMALL and call(ws=None) == INVALID and call(ws=64 * MB + 8) == INVALID
+    assert need > 0 and aq.wush_lora_workspace_bytes(256, 256, 512, 4, 16) == 0
+    assert call(wn=need - 1) == TOO_SMALL and call(ws=None) == INVALID and call(ws=64 * MB + 8) == INVALID
+    for at in (1 * MB, 16 * MB, 32 * MB, 32 * MB - 512):                  # on x, y_in and y
+        assert call(ws=at) == INVALID, at
     for bad in ((-1, 256, 512, 4, 16), (0, 256, 512, 4, 16), (10, 0, 512, 4, 16), (10, 256, 512, 0, 16)):
         assert aq.wush_lora_workspace_bytes(*bad) == 0
 
