@@ -478,7 +478,7 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* warp_sums, 
 
 // One CTA.  ORDERED: an adapter's tokens keep their order, so that the rows of a request lie
 // side by side in a tile and shrink can fetch them in blocks: every warp has a stretch of the
-// tokens and counters of its own, in shared memory [32][n + 1].  Otherwise (pools of more
+// tokens and counters of its own, in shared memory [32][n + 1], with a row of sums behind them.  Otherwise (pools of more
 // than kOrderedAdapters) there is one set of counters, and the order is left to the atomics;
 // a token's result is the same in every place of a tile, since rows of an MMA do not meet and
 // everything else is per row.
@@ -493,6 +493,7 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const int32_t* 
   constexpr int kSets = ORDERED ? 32 : 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int* mine = count + (ORDERED ? warp * (n + 1) : 0);
+  int* start = count + (ORDERED ? 32 * (n + 1) : 0);       // adapters' totals, then their first slots
   for (int i = tid; i < kSets * (n + 1); i += kPlanThreads) count[i] = 0;
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
@@ -529,12 +530,25 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const int32_t* 
     }
   }
   __syncthreads();
+  // Each adapter's total and the warps' places within it (ORDERED): a warp for an adapter, a
+  // lane for a warp's counter.
+  if (ORDERED) {
+    for (int i = warp; i <= n; i += 32) {
+      const int c = count[lane * (n + 1) + i];
+      int x = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      count[lane * (n + 1) + i] = x - c;
+      if (lane == 31) start[i] = x;
+    }
+    __syncthreads();
+  }
   uint64_t base = 0;
   for (int i0 = 0; i0 <= n; i0 += kPlanThreads) {
-    const int i = i0 + tid;
-    int c = 0;
-    if (i <= n)
-      for (int q = 0; q < kSets; ++q) c += count[q * (n + 1) + i];
+    const int i = i0 + tid, c = i <= n ? start[i] : 0;
     const int k = i >= n ? 0 : i0 == 0 ? my_rank : rank_of(i), tiles = (c + kTile - 1) / kTile;
     uint64_t all;
     const uint64_t at = base + block_scan(uint64_t(c) << 32 | uint64_t(tiles), warp_sums, &all);
@@ -554,14 +568,7 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const int32_t* 
       const int t2 = __shfl_sync(0xffffffffu, tile, of), nt = __shfl_sync(0xffffffffu, tiles, of);
       for (int j = lane; j < nt; j += 32) cut(t2, i2, f2, c2, k2, j);
     }
-    if (c) {
-      int slot = first;
-      for (int q = 0; q < kSets; ++q) {
-        const int here = count[q * (n + 1) + i];
-        count[q * (n + 1) + i] = slot;
-        slot += here;
-      }
-    }
+    if (i <= n) start[i] = first;
   }
   if (tid == 0) *w.counts = Counts{static_cast<int>(base), 0u};
   __syncthreads();
@@ -578,6 +585,7 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const int32_t* 
         if (ORDERED) {
           at = mine[g];
           mine[g] = at + __popc(same);
+          at += start[g];
         } else {
           at = atomicAdd(&mine[g], __popc(same));
         }
@@ -1226,11 +1234,11 @@ int launch_many(const LoraArgs& p, const Work& w, cudaStream_t st) {
     return WUSH_ERR_CUDA;
   const int64_t tiles = max_tiles(p.tokens, p.n_adapters);
   const bool ordered = p.n_adapters <= kOrderedAdapters;
-  const int plan_smem = (p.n_adapters + 1) * 4 * (ordered ? 32 : 1);
+  const int plan_smem = (p.n_adapters + 1) * 4 * (ordered ? 33 : 1);
   auto plan = ordered ? lora_plan_kernel<true> : lora_plan_kernel<false>;
   if (plan_smem > 48 * 1024 - 256) {
     static std::atomic<uint64_t> done[2] = {{0}, {0}};
-    const int most = ordered ? (kOrderedAdapters + 1) * 128 : (kPlanAdapters + 1) * 4;
+    const int most = ordered ? (kOrderedAdapters + 1) * 33 * 4 : (kPlanAdapters + 1) * 4;
     if (set_smem_once(plan, most, done[ordered]) != WUSH_OK) return WUSH_ERR_CUDA;
   }
   int rc = launch_pdl(plan, 1, kPlanThreads, plan_smem, st, p.adapter, p.tokens, p.n_adapters, p.rank, p.ranks, w);
