@@ -135,34 +135,35 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// Asks for the 128-byte lines of [p, p + bytes) to be brought into L2, by the CTA's threads.
-__device__ __forceinline__ void prefetch_l2(const void* p, int64_t bytes) {
-  for (int64_t i = threadIdx.x * int64_t(128); i < bytes; i += kFewThreads * 128)
+// Asks for the 128-byte lines of [p, p + bytes) to be brought into L2, by ``threads`` threads
+// of which this is number ``i0``.
+__device__ __forceinline__ void prefetch_l2(const void* p, int64_t bytes, int i0, int threads) {
+  for (int64_t i = i0 * int64_t(128); i < bytes; i += threads * 128)
     asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) + i));
 }
 
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
 }
 
 // MB: blocks of 16 ranks held at once.  Shared memory: the warps' partial s
-// [8][MB * 16][8], this CTA's sum [MB * 16][8], the terms [kTerms][8][MB * 16 + 8].
+// [8][MB * 16][8], the CTAs' sums [8][MB * 16][8], the terms [kTerms][8][MB * 16 + 8].
 //
 // What bounds it is latency: of the adapter's number, of A and x, of the cluster's meeting,
-// of B.  So B is on its way into L2 while s is computed, a warp asks for all of a step's A and
-// for several blocks of B (kUnroll) before it multiplies any, and the CTAs part from the
-// cluster when they have read each other's sums, not at their end.  (16 tokens, 4096 x 4096,
-// rank 64, one adapter each: 10.5 us; without the three 12.7 us.)
+// of B.  So B and y_in are on their way into L2 while s is computed, a warp asks for all of a
+// step's A and for several blocks of B (kUnroll) before it multiplies any, and a CTA writes its
+// sums to the others before they meet, so that nobody reads across after it.  (16 tokens, 4096 x
+// 4096, rank 64, one adapter each: 9.8 us; without these 12.7 us.)
 template <typename E, int MB>
-__global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const __grid_constant__ LoraArgs p) {
+__global__ void __launch_bounds__(kFewThreads, MB <= 2 ? 3 : MB <= 8 ? 2 : 1)
+    lora_few_kernel(const __grid_constant__ LoraArgs p) {
   constexpr int kR = MB * 16, kT = Split<E>::kTerms, kRow = kR + 8;
   constexpr int kUnroll = MB <= 2 ? 4 : MB <= 4 ? 2 : 1;
   extern __shared__ __align__(16) unsigned char smem[];
   float* part = reinterpret_cast<float*>(smem);
-  float* mine = part + kFewWarps * kR * 8;
-  E* terms = reinterpret_cast<E*>(mine + kR * 8);
+  float* parts = part + kFewWarps * kR * 8;                // written by the CTAs of the cluster
+  E* terms = reinterpret_cast<E*>(parts + kCluster * kR * 8);
   __shared__ int s_tok[8], s_warp[kFewWarps];
   __shared__ float s_up[8];
 
@@ -233,24 +234,33 @@ __global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const __grid_cons
   const int blocks = (p.d_out + 15) / 16, per = (blocks + kCluster - 1) / kCluster;
   const int nb_first = cta * per < blocks ? cta * per : blocks, nb_last = nb_first + per < blocks ? nb_first + per : blocks;
   const int n_last = nb_last * 16 < p.d_out ? nb_last * 16 : p.d_out;
-  prefetch_l2(B + static_cast<int64_t>(nb_first) * 16 * p.rank, static_cast<int64_t>(n_last - nb_first * 16) * p.rank * 2);
+  cluster_arrive();                                        // this CTA runs: the others may write to it
+  prefetch_l2(B + static_cast<int64_t>(nb_first) * 16 * p.rank, static_cast<int64_t>(n_last - nb_first * 16) * p.rank * 2,
+              tid, kFewThreads);
   __syncthreads();
+  if (p.y_in && s_tok[warp] >= 0 && nb_first < nb_last)
+    prefetch_l2(p.y_in + s_tok[warp] * p.y_in_stride + nb_first * 16, static_cast<int64_t>(n_last - nb_first * 16) * 4, lane, 32);
 
   // s = A x, split over d_in between the 64 warps of the cluster
   const E* A = static_cast<const E*>(p.a) + static_cast<int64_t>(g) * p.rank * p.d_in;
   const int my_tok = s_tok[row];
   const E* x = my_tok >= 0 ? static_cast<const E*>(p.x) + my_tok * p.x_stride : nullptr;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  float acc[MB][4] = {}, sum[MB][4] = {};
-  int steps = 0;
-  for (int kb = cta * kFewWarps + warp; kb < p.d_in / 32; kb += kCluster * kFewWarps) {
-    if (steps++ == 16) {                                   // (chains of 32 MMAs: see kChain)
-      steps = 1;
+  float acc[MB][4] = {};
+  // (chains of 32 MMAs: see kChain; the warp's part is its lanes' own places)
+  auto flush = [&](bool fresh) {
 #pragma unroll
-      for (int m = 0; m < MB; ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sum[m][j] += acc[m][j], acc[m][j] = 0.0f;
+    for (int m = 0; m < MB; ++m) {
+      float2* o = reinterpret_cast<float2*>(part + (warp * kR + m * 16 + row) * 8 + c * 2);
+      const float2 u = fresh ? make_float2(0.0f, 0.0f) : o[0], v = fresh ? make_float2(0.0f, 0.0f) : o[32];
+      o[0] = make_float2(u.x + acc[m][0], u.y + acc[m][1]);
+      o[32] = make_float2(v.x + acc[m][2], v.y + acc[m][3]);
+      acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.0f;
     }
+  };
+  int steps = 0;
+  for (int kb = cta * kFewWarps + warp; kb < p.d_in / 32; kb += kCluster * kFewWarps, ++steps) {
+    if (steps && steps % 16 == 0) flush(steps == 16);
     const int col = kb * 32 + c * 8;
     const uint4 xv = x ? *reinterpret_cast<const uint4*>(x + col) : zero;
     uint4 lo[MB], hi[MB];
@@ -266,14 +276,11 @@ __global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const __grid_cons
       mma16816<E>(acc[m], lo[m].z, hi[m].z, lo[m].w, hi[m].w, xv.z, xv.w);
     }
   }
-#pragma unroll
-  for (int m = 0; m < MB; ++m) {
-    float* o = part + (warp * kR + m * 16 + row) * 8 + c * 2;
-    *reinterpret_cast<float2*>(o) = make_float2(sum[m][0] + acc[m][0], sum[m][1] + acc[m][1]);
-    *reinterpret_cast<float2*>(o + 64) = make_float2(sum[m][2] + acc[m][2], sum[m][3] + acc[m][3]);
-  }
+  flush(steps <= 16);
   __syncthreads();
+  cluster_wait();
   const int used = (k + 15) / 16 * 16 * 8;                 // of s, [rank][token]
+  const uint32_t to = sm100::smem_u32(parts + cta * kR * 8);
   for (int i = tid * 4; i < used; i += kFewThreads * 4) {
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -281,27 +288,24 @@ __global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const __grid_cons
       const float4 q = *reinterpret_cast<const float4*>(part + w * kR * 8 + i);
       s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
     }
-    *reinterpret_cast<float4*>(mine + i) = s;
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r) st_cluster4(sm100::mapa_shared(to + i * 4, r), s);
   }
   cluster_arrive();
   cluster_wait();
   // every CTA sums the eight CTAs' parts, in their order
   const float sc = p.scale ? p.scale[g] : 1.0f;
   float* total = part;                                     // [kR][8], the warps' parts are done with
-  const uint32_t base = sm100::smem_u32(mine);
   for (int i = tid * 4; i < used; i += kFewThreads * 4) {
-    float4 q[kCluster];
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int r = 0; r < kCluster; ++r) q[r] = ld_cluster4(sm100::mapa_shared(base + i * 4, r));
-    float4 s = q[0];
-#pragma unroll
-    for (int r = 1; r < kCluster; ++r) {
-      s.x += q[r].x; s.y += q[r].y; s.z += q[r].z; s.w += q[r].w;
+    for (int r = 0; r < kCluster; ++r) {
+      const float4 q = *reinterpret_cast<const float4*>(parts + r * kR * 8 + i);
+      s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
     }
     *reinterpret_cast<float4*>(total + i) = make_float4(s.x * sc, s.y * sc, s.z * sc, s.w * sc);
   }
   __syncthreads();
-  cluster_arrive();                                        // waited for at the end: others may read this CTA's sums yet
   // a warp for each token: its s, scaled (fp16) and split
   {
     float down = 1.0f, up = 1.0f;
@@ -371,13 +375,12 @@ __global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const __grid_cons
       }
     }
   }
-  cluster_wait();                                          // no CTA leaves while another may read its sums
 }
 
 template <typename E, int MB>
 int launch_few(const LoraArgs& p, cudaStream_t st) {
   constexpr int kR = MB * 16;
-  constexpr int smem = kFewWarps * kR * 8 * 4 + kR * 8 * 4 + Split<E>::kTerms * 8 * (kR + 8) * 2;
+  constexpr int smem = (kFewWarps + kCluster) * kR * 8 * 4 + Split<E>::kTerms * 8 * (kR + 8) * 2;
   auto kern = lora_few_kernel<E, MB>;
   if (smem > 48 * 1024 - 256) {
     static std::atomic<uint64_t> done{0};
@@ -1254,7 +1257,7 @@ int launch_many(const LoraArgs& p, const Work& w, cudaStream_t st) {
 
 // Few tokens (or a pool too large to count in shared memory, or for a tensor map) go through
 // the cluster kernel, whose clusters each look through the adapters of all tokens.  Measured on
-// both sides: 200 tokens on 48 adapters, 4096 x 12288, rank 32: 31.5 us, 56 us by the three
+// both sides: 200 tokens on 48 adapters, 4096 x 12288, rank 32: 31.1 us, 56 us by the three
 // launches; 276 tokens on one adapter, 352 x 4616, rank 128: 24.7 and 25.2 us; 391 tokens on one
 // adapter, 576 x 5296, rank 96: 37.6 and 23.0 us.
 constexpr int kFewTokens = 256;
