@@ -446,15 +446,17 @@ def itq3_dequant_gemv_noalloc(codes, scales, x, d_out: int, y, stream=None):
 
 
 _DTYPES = {}
-_raw_stream = None
+_raw_stream = _current_device = None
 
 
 def _device_call(t):
     """The device of a CUDA tensor (an index): what the other tensors of a call are compared with."""
-    global _raw_stream
+    global _raw_stream, _current_device
     if _raw_stream is None:
         import torch
         _DTYPES.update({torch.bfloat16: 0, torch.float32: 1, torch.float16: 2})
+        # torch's own short cuts, where it has them: these calls take microseconds in all
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda dev: torch.cuda.current_stream(dev).cuda_stream)
     return t.get_device()
@@ -471,8 +473,10 @@ def _rows(fn, name, t, shape, dev):
         raise ValueError(f"{fn}: {name} must be {tuple(shape)}, got {tuple(t.shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{fn}: {name} is on {t.device}, another tensor on {'cpu' if dev < 0 else f'cuda:{dev}'}")
-    row_stride, col_stride = t.stride()
     rows, d = shape
+    if t.is_contiguous():
+        return t.data_ptr(), dt, d
+    row_stride, col_stride = t.stride()
     if d > 1 and col_stride != 1:
         raise ValueError(f"{fn}: the rows of {name} must be contiguous")
     if rows <= 1:
@@ -508,15 +512,15 @@ def _norm_spec(fn, which, kind, weight, bias, d, dev, eps, weight_offset):
 
 def _launch(fn, name, args, dev, stream):
     """Calls ``fn(*args, stream)`` with device ``dev`` current, on its current stream unless one is given."""
-    import torch
     if dev < 0:
         raise ValueError("expected a CUDA tensor")
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
+        import torch
         with torch.cuda.device(dev):
             status = fn(*args, _stream(stream))
     else:
         status = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
-    if status != 0:
+    if status:
         raise WushError(name, status)
 
 

@@ -42,6 +42,7 @@ using sm100::mbar_init;
 
 constexpr int kMaxWidth = 32768;
 constexpr int kMaxStages = 4;
+constexpr int64_t kFewRows = 296;                           // two a SM
 constexpr int kMinThreads = 128;                           // few rows: narrow ones share a CTA of this many threads
 constexpr int64_t kDefaultPolls = int64_t(1) << 40;        // waits end on the timer
 constexpr uint64_t kDeadlineNs = 4000000000ull;
@@ -600,16 +601,12 @@ bool shifted(Args* a) {
 int round_up(int n, int m) { return (n + m - 1) / m * m; }
 
 int run(Args& a, bool vec, cudaStream_t st) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return WUSH_ERR_CUDA;
   const int groups = (a.d + 7) / 8;
   a.inv_d = 1.0f / static_cast<float>(a.d);
   // Few rows, or narrow ones: the ring's set-up would cost more than it hides.  Measured: 7696
   // rows of 174, 16 bits: 4.9 us and 29 us by the ring; 5536 of 1216, fp32 y, layer norm, gate:
   // 24.9 and 35.5 us; 4096 of 4096, fp32 y: 38.7 and 29.0 us.
-  if ((a.rows <= 2 * sms && groups <= 1024) || groups <= 256) {
+  if ((a.rows <= kFewRows && groups <= 1024) || groups <= 256) {
     int threads = round_up(groups, 32);
     if (threads < kMinThreads) threads = threads <= 32 ? 32 : threads <= 64 ? 64 : kMinThreads;
     a.row_threads = threads;
@@ -618,6 +615,10 @@ int run(Args& a, bool vec, cudaStream_t st) {
     return vec ? launch_pdl(norm_few_kernel<kAligned>, static_cast<unsigned>(grid), block, 0, st, a)
                : launch_pdl(norm_few_kernel<kScalar>, static_cast<unsigned>(grid), block, 0, st, a);
   }
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return WUSH_ERR_CUDA;
   if (vec) return launch_width<kAligned>(a, sms, st);
   if (shifted(&a)) {
     const int rc = launch_width<kShifted>(a, sms, st);
