@@ -2,17 +2,18 @@
 //   y[t] = y_in[t] + scale[g] * B_g (A_g x[t]),   g = adapter[t].
 //
 // Tokens of one adapter are taken together, so that its matrices are read once for
-// up to eight tokens.  Both products run as m16n8k16 MMAs with the adapter's matrix
-// as the 16-row operand and the tokens as the 8 columns: the matrices go from global
-// memory straight into MMA fragments (the order of k inside a step is free as long
-// as both operands share it, so a lane takes 16 consecutive bytes of a row).
+// up to eight of them (few tokens) or 64 (many).
 //
 // Precision.  The products of 16-bit inputs are exact in fp32 and s = A x is kept in
-// fp32; for the second product s is split into 16-bit terms whose sum carries at
-// least 22 bits of it, so what rounds is the fp32 accumulation:
-//   bf16: three bf16 terms (8 bits each, the range of fp32);
-//   fp16: two fp16 terms (11 bits each) after a power-of-two scaling of the token's
-//         s to below 1, undone exactly on the result.
+// fp32; for the second product s is split into 16-bit terms, so that what rounds is the
+// fp32 accumulation:
+//   bf16: three bf16 terms, each what the ones before it leave cut to 8 bits: all 24 bits
+//         of s, and no finite s becomes an infinity;
+//   fp16: two fp16 terms (11 bits each) after a power-of-two scaling of the token's s to
+//         below 1, undone exactly on the result.  The second term is held times 2^24 and
+//         has a sum of its own, since beside the first it would lie in fp16's subnormals
+//         for all but the largest s: 23 bits of an s down to 2^-14 of the token's largest,
+//         12 bits at 2^-25 and on to 2^-38.
 #include <type_traits>
 
 #include "rowops.cuh"
@@ -81,24 +82,27 @@ template <typename E>
 struct Split;
 template <>
 struct Split<__nv_bfloat16> {
-  static constexpr int kTerms = 3;
+  static constexpr int kTerms = 3, kSums = 1;              // kSums: sums that the terms' products go to
 };
 template <>
 struct Split<__half> {
-  static constexpr int kTerms = 2;
+  static constexpr int kTerms = 2, kSums = 2;
 };
+constexpr float kUpSecond = 16777216.0f, kDownSecond = 1.0f / kUpSecond;  // of fp16's second term
 
-// The 16-bit terms of v; each is the nearest value to what the ones before it leave.
+// The 16-bit terms of v.  (An infinity is its own first term and leaves nothing.)
 template <typename E>
 __device__ __forceinline__ void split(float v, E (&t)[Split<E>::kTerms]) {
 #pragma unroll
   for (int i = 0; i < Split<E>::kTerms; ++i) {
     if constexpr (std::is_same<E, __half>::value) {
       t[i] = __float2half_rn(v);
-      v -= __half2float(t[i]);
+      const float got = __half2float(t[i]);
+      v = v == got ? 0.0f : (v - got) * kUpSecond;
     } else {
-      t[i] = __float2bfloat16_rn(v);
-      v -= __bfloat162float(t[i]);
+      t[i] = __float2bfloat16_rz(v);
+      const float got = __bfloat162float(t[i]);
+      v = v == got ? 0.0f : v - got;
     }
   }
 }
@@ -116,13 +120,19 @@ __device__ __forceinline__ void fp16_scaling(float top, float* down, float* up) 
   }
 }
 
+// |v| for fp16_scaling's ``top``: the largest finite magnitude.
+__device__ __forceinline__ float finite_magnitude(float v) { return fabsf(v) < INFINITY ? fabsf(v) : 0.0f; }
+
 __device__ __forceinline__ uint32_t keep_below(uint32_t pair, int col, int k) {   // elements col, col + 1
   return col + 1 < k ? pair : col < k ? pair & 0xffffu : 0u;
 }
 
 // ---------------------------------------------------------------------------
 // Few tokens: one cluster of eight CTAs takes up to eight tokens of one adapter
-// through both products in one launch.
+// through both products in one launch.  Both run as m16n8k16 MMAs with the adapter's
+// matrix as the 16-row operand and the tokens as the 8 columns: the matrices go from
+// global memory straight into MMA fragments (the order of k inside a step is free as long
+// as both operands share it, so a lane takes 16 consecutive bytes of a row of A, 8 of B).
 // ---------------------------------------------------------------------------
 constexpr int kCluster = 8, kFewThreads = 256, kFewWarps = kFewThreads / 32;
 
@@ -311,7 +321,7 @@ __global__ void __launch_bounds__(kFewThreads, MB <= 2 ? 3 : MB <= 8 ? 2 : 1)
     float down = 1.0f, up = 1.0f;
     if (std::is_same<E, __half>::value) {
       float top = 0.0f;
-      for (int r = lane; r < used / 8; r += 32) top = fmaxf(top, fabsf(total[r * 8 + warp]));
+      for (int r = lane; r < used / 8; r += 32) top = fmaxf(top, finite_magnitude(total[r * 8 + warp]));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       fp16_scaling(top, &down, &up);
@@ -353,7 +363,7 @@ __global__ void __launch_bounds__(kFewThreads, MB <= 2 ? 3 : MB <= 8 ? 2 : 1)
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int n0 = (nb + u) * 16 + row, n1 = n0 + 8;
-      float o[4] = {};
+      float o[Split<E>::kSums][4] = {};
 #pragma unroll
       for (int m = 0; m < MB; ++m) {
         const int col = m * 16 + c * 4;
@@ -364,14 +374,15 @@ __global__ void __launch_bounds__(kFewThreads, MB <= 2 ? 3 : MB <= 8 ? 2 : 1)
 #pragma unroll
         for (int q = 0; q < kT; ++q) {
           const uint2 s = *reinterpret_cast<const uint2*>(terms + (q * 8 + row) * kRow + col);
-          mma16816<E>(o, a0, a1, a2, a3, s.x, s.y);
+          mma16816<E>(o[q % Split<E>::kSums], a0, a1, a2, a3, s.x, s.y);
         }
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int n = j < 2 ? n0 : n1, tok = j & 1 ? tok1 : tok0;
+        const float sum = std::is_same<E, __half>::value ? fmaf(o[Split<E>::kSums - 1][j], kDownSecond, o[0][j]) : o[0][j];
         if (tok >= 0 && nb + u < nb_last && n < p.d_out)
-          p.y[tok * p.y_stride + n] = fmaf(o[j], j & 1 ? up1 : up0, old[u][j]);
+          p.y[tok * p.y_stride + n] = fmaf(sum, j & 1 ? up1 : up0, old[u][j]);
       }
     }
   }
@@ -665,8 +676,8 @@ constexpr int kBk = 128;                                  // columns of d_in a s
 // rounding of the sums (4096 tokens x 12288, rank 128: a chain over a CTA's whole d_in gave
 // 2.8e-6 relative to the result, chains of 32 give 1.0e-6).
 //
-// (Copies by cp.async would have to pass a proxy fence before the MMAs may read them, and
-// that fence waits for the copies still in flight too: 30 us at 4096 tokens x 12288, rank 64.)
+// What bounds it: 4096 tokens x 12288, rank 64, read 113 MB from DRAM and 282 MB from L2 (A
+// once a tile) in some 31 us, the tensor pipe active for a quarter of it.
 constexpr int kChain = 4;
 
 template <int R>
@@ -737,8 +748,8 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __gri
   const uint32_t ranks16 = (k + 15) / 16 * 16;             // columns of D that the MMAs compute
   float total[R / 8][4] = {};
   if (warp == 4) {
-    // lane: half of the stage, eight rows of x: one block where they follow one another (TMA
-    // takes rows so four times as fast as gathered ones), else two gathers (rows without a token
+    // lane: half of the stage, eight rows of x: one block where they follow one another
+    // (4096 tokens x 12288, rank 64: 31.6 us, 40.7 us with all rows gathered), else two gathers (rows without a token
     // lie beyond x and read as zero; groups without one are left as they are)
     const int half = (lane >> 3) & 1, row = (lane & 7) * 8, none = static_cast<int>(p.tokens);
     const int groups = (count + 7) / 8;
@@ -849,7 +860,7 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __gri
         for (int q = 0; q < 8; ++q) v[i] += part[q];
         v[i] *= sc;
       }
-      top = fmaxf(top, fabsf(v[i]));
+      top = fmaxf(top, finite_magnitude(v[i]));
     }
     float down = 1.0f, up = 1.0f;
     if (std::is_same<E, __half>::value) {
@@ -881,9 +892,12 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __gri
 // bit 1 clear and block 1 the others (TMA gathers B's rows in that order), so that a thread's
 // values of both blocks are four consecutive columns: one 16-byte access of y each.
 //
-// One warp asks for the terms and B, one issues the MMAs, eight add D to y_in and store.  These
-// fetch their own y_in, by asynchronous copies into slots that only the thread itself reads, so
-// the roles meet on barriers in shared memory alone.
+// One warp asks for the terms and B, one issues the MMAs, one draws pieces of work, eight add D
+// to y_in and store.  These fetch their own y_in, by asynchronous copies into slots that only the
+// thread itself reads, so the roles meet on barriers in shared memory alone.
+//
+// What bounds it: y_in and y, which pass once.  8192 tokens x 17408, rank 16: 1.11 GB of DRAM
+// traffic in 203 us, 5.5 TB/s.
 constexpr int kExpandThreads = 352;
 constexpr int kAddThreads = 256;
 
@@ -905,16 +919,20 @@ Expand expand_layout(int row_elems) {
     if (left >= y) ++l.y_slots, left -= y;
   }
   l.smem = l.terms_bytes + l.b_slots * l.b_bytes + l.y_slots * y + 1024;
+  // (a CTA's share of TMEM, 256 columns of 512 for fp16, is no larger than its share of shared
+  // memory: see Shrink)
+  if (l.smem < 112 * 1024 && Split<E>::kSums > 1) l.smem = 112 * 1024;
   return l;
 }
 
 template <typename E>
-__global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const __grid_constant__ LoraArgs p,
+__global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __grid_constant__ LoraArgs p,
                                                                      const __grid_constant__ Work w,
                                                                      const __grid_constant__ Expand l,
                                                                      const __grid_constant__ CUtensorMap map_s,
                                                                      const __grid_constant__ CUtensorMap map_b) {
-  constexpr int kT = Split<E>::kTerms, kSlot = kTile * kCols * 4;
+  constexpr int kT = Split<E>::kTerms, kSums = Split<E>::kSums, kSlot = kTile * kCols * 4;
+  constexpr int kD = kSums * kCols;                        // columns of TMEM that one D takes, of two in turn
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t b_full[4], b_empty[4], d_full[2], d_empty[2], s_full, s_empty, piece_full[2],
       piece_empty[2];
@@ -944,7 +962,7 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const __gri
     sm100::prefetch_tmap(&map_b);
   }
   __syncwarp();
-  if (warp == 8) sm100::tmem_alloc(&tmem_slot, 2 * kCols);
+  if (warp == 8) sm100::tmem_alloc(&tmem_slot, 2 * kD);
   sm100::tc_fence_before();
   __syncthreads();
   sm100::tc_fence_after();
@@ -1052,8 +1070,9 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const __gri
           for (int t = 0; t < kT; ++t)
             for (int ks = 0; ks < kp; ks += 16) {
               const int pos_k = t * w.row_elems + ks;
-              tc_mma(tmem + d * kCols, s_base + (pos_k >> 6) * (kTile * 128) + (pos_k & 63) * 2,
-                     at + (ks >> 6) * (kCols * 128) + (ks & 63) * 2, idesc, t + ks > 0);
+              tc_mma(tmem + d * kD + t % kSums * kCols, s_base + (pos_k >> 6) * (kTile * 128) + (pos_k & 63) * 2,
+                     at + (ks >> 6) * (kCols * 128) + (ks & 63) * 2, idesc,
+                     t >= kSums || ks > 0);
             }
           sm100::tc_commit(&b_empty[s]);
           sm100::tc_commit(&d_full[d]);
@@ -1109,8 +1128,20 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const __gri
             sm100::tc_fence_after();
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              tmem_ld_16x8(tmem + (static_cast<uint32_t>(wm * 32) << 16) + d * kCols + wn * 32 + j * 8, acc[j]);
-            sm100::tmem_ld_wait();
+              tmem_ld_16x8(tmem + (static_cast<uint32_t>(wm * 32) << 16) + d * kD + wn * 32 + j * 8, acc[j]);
+            if constexpr (kSums == 2) {
+              float low[4][4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                tmem_ld_16x8(tmem + (static_cast<uint32_t>(wm * 32) << 16) + d * kD + kCols + wn * 32 + j * 8, low[j]);
+              sm100::tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(low[j][e], kDownSecond, acc[j][e]);
+            } else {
+              sm100::tmem_ld_wait();
+            }
             sm100::tc_fence_before();
           }
           __syncwarp();
@@ -1142,7 +1173,7 @@ __global__ void __launch_bounds__(kExpandThreads) lora_expand_kernel(const __gri
   __syncthreads();
   if (warp == 8) {
     sm100::tc_fence_after();
-    sm100::tmem_dealloc(tmem, 2 * kCols);
+    sm100::tmem_dealloc(tmem, 2 * kD);
   }
   if (tid == 0 && *static_cast<volatile int*>(&abort_flag)) report_timeout();
 }

@@ -506,10 +506,12 @@ int wush_norm(const void* x, int x_dtype, int64_t x_stride, int64_t rows, int64_
  *   y[t, o] = y_in[t, o] + scale[g] * sum_{j < k_g} s[t, j] b[g, o, j]
  * and y[t] = y_in[t] where g is outside [0, n_adapters) (no adapter; -1 by
  * convention) or k_g is 0.  Products are exact, sums are fp32, and s enters the
- * second product with at least 22 bits.  A token's result does not depend on which
+ * second product with all its bits (bf16) or with 23 of them down to 2^-14 of the
+ * token's largest |s|, fewer below (fp16).  A token's result does not depend on which
  * other tokens share the call beyond fp32 rounding, and equal calls give equal bits.
  * A NaN or an infinity in a token's x or y_in reaches that token only, one in an
- * adapter that adapter's tokens only.
+ * adapter that adapter's tokens only; an infinite s counts as the formula says, an
+ * infinity in b may give NaN in its place.
  *
  * x:        device [tokens, d_in], bf16 or fp16 (dtype), row stride x_stride (in
  *           elements, a multiple of 8).
@@ -523,9 +525,9 @@ int wush_norm(const void* x, int x_dtype, int64_t x_stride, int64_t rows, int64_
  * y:        device fp32 [tokens, d_out], row stride a multiple of 4; may be y_in (with
  *           its stride), otherwise it may overlap neither y_in nor x.
  * workspace: device, at least wush_lora_workspace_bytes(...) bytes, 16-byte aligned, apart
- *           from x, y_in and y; may be NULL where that is 0 (256 tokens or fewer).  Calls that can overlap in time (two streams,
- *           two graphs) need one each.
- *           What it holds before and after a call is of no meaning.
+ *           from x, y_in and y; may be NULL where that is 0 (256 tokens or fewer).  Calls
+ *           that can overlap in time (two streams, two graphs) need one each.  What it
+ *           holds before and after a call is of no meaning.
  * Requirements: 0 <= tokens <= 2^24 (0: nothing is launched), d_in % 32 == 0,
  * d_out % 8 == 0, both <= 2^24, rank % 8 == 0, 8 <= rank <= 256, n_adapters <= 2^20; with
  * n_adapters > 57344 or n_adapters * d_out >= 2^31, tokens <= 4096.

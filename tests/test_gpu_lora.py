@@ -236,3 +236,40 @@ def test_a_pool_too_large_to_count_in_shared_memory(lib):
 @pytest.mark.parametrize("tokens", [2, 300])
 def test_a_long_reduction(lib, tokens):
     check(lib, tokens, 1 << 17, 64, 2, 8)
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("tokens", [3, 300])
+def test_an_infinity_in_a_factor_counts_as_the_formula_says(lib, tokens, dt):
+    # s of rank 0 is an infinity, the others' are beyond fp16's range: y is the infinity's sign times b's
+    torch.manual_seed(tokens)
+    x = torch.rand(tokens, 64, device="cuda").to(dt) + 0.5
+    a, b = pool(2, 16, 64, 40, dt)
+    a[1, 0, 5] = float("inf")
+    adapter = (torch.arange(tokens, device="cuda") % 2).to(torch.int32)
+    sc = torch.tensor([1.0, 1e6], device="cuda")
+    ws = torch.empty(max(16, lib.wush_lora_workspace_bytes(tokens, 64, 40, 2, 16)), dtype=torch.uint8, device="cuda")
+    y = torch.empty(tokens, 40, device="cuda")
+    lib.wush_lora_add(x, adapter, a, b, None, y, ws, None, sc)
+    assert bool(torch.isfinite(y[::2]).all())
+    assert torch.equal(y[1::2], (float("inf") * torch.sign(b[1, :, 0].float())).expand_as(y[1::2]))
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("tokens", [5, 300])
+def test_small_ranks_beside_large_ones(lib, tokens, dt):
+    # Rank j's s is some 2^-j of rank 0's, and row o of b uses rank o % 15 alone.  All terms of a
+    # sum are positive, so that every rounding is relative to the result itself: the 80 steps of
+    # 2^-23 above, the split of s (2^-24 down to 2^-14 of the largest) among them.
+    torch.manual_seed(tokens)
+    x = torch.rand(tokens, 256, device="cuda").to(dt) + 0.5
+    a = ((torch.rand(1, 16, 256, device="cuda") + 0.5) * 2.0 ** -torch.arange(16, device="cuda")[:, None]).to(dt)
+    o = torch.arange(120, device="cuda")
+    b = torch.zeros(1, 120, 16, device="cuda", dtype=dt)
+    b[0, o, o % 15] = (torch.rand(120, device="cuda") + 0.5).to(dt)
+    ws = torch.empty(max(16, lib.wush_lora_workspace_bytes(tokens, 256, 120, 1, 16)), dtype=torch.uint8, device="cuda")
+    y = torch.empty(tokens, 120, device="cuda")
+    lib.wush_lora_add(x, torch.zeros(tokens, dtype=torch.int32, device="cuda"), a, b, None, y, ws)
+    want = (x.double() @ a[0].double().T) @ b[0].double().T
+    err = (y.double() - want).abs()
+    assert bool((err <= 80 * 2 * U * want).all()), float((err / want).max())
