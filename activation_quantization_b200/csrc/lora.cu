@@ -160,71 +160,94 @@ __device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v) {
 // MB: blocks of 16 ranks held at once.  Shared memory: the warps' partial s
 // [8][MB * 16][8], the CTAs' sums [8][MB * 16][8], the terms [kTerms][8][MB * 16 + 8].
 //
-// What bounds it is latency: of the adapter's number, of A and x, of the cluster's meeting,
-// of B.  So B and y_in are on their way into L2 while s is computed, a warp asks for all of a
-// step's A and for several blocks of B (kUnroll) before it multiplies any, and a CTA writes its
-// sums to the others before they meet, so that nobody reads across after it.  (16 tokens, 4096 x
-// 4096, rank 64, one adapter each: 9.8 us; without these 12.7 us.)
+// What bounds it is latency: of the adapter's number, of A and x, of the cluster's meeting, of B.
+// So no load hides behind a branch (what is not there reads something that is): all of a step's
+// are in flight before any is used.  B and y_in are on their way into L2 while s is computed, a
+// warp asks for several blocks of B (kUnroll) before it multiplies any, and a CTA writes its sums
+// to the others before they meet, so that nobody reads across after it.  1 token, 4096 x 4096,
+// rank 16: 4.1 us, of which about 0.5 go to the adapter's number, 0.5 to the grouping, 0.6 to A,
+// 1.2 to the sums and terms, 0.9 to B and y.  16 tokens, 4096 x 4096, rank 64, one adapter each:
+// 8.9 us, 2.1 TB/s; 48 of rank 32, 4096 x 12288: 18.0 us, 3.1 TB/s.
+constexpr int few_ctas(int mb) { return mb <= 2 ? 3 : mb <= 8 ? 2 : 1; }   // an SM
+
 template <typename E, int MB>
-__global__ void __launch_bounds__(kFewThreads, MB <= 2 ? 3 : MB <= 8 ? 2 : 1)
+__global__ void __launch_bounds__(kFewThreads, few_ctas(MB))
     lora_few_kernel(const __grid_constant__ LoraArgs p) {
   constexpr int kR = MB * 16, kT = Split<E>::kTerms, kRow = kR + 8;
-  constexpr int kUnroll = MB <= 2 ? 4 : MB <= 4 ? 2 : 1;
+  constexpr int kUnroll = MB == 1 ? 4 : MB == 2 ? 3 : MB <= 4 ? 2 : 1, kSteps = MB <= 2 ? 2 : 1;   // blocks of B, steps of A in flight
   extern __shared__ __align__(16) unsigned char smem[];
   float* part = reinterpret_cast<float*>(smem);
   float* parts = part + kFewWarps * kR * 8;                // written by the CTAs of the cluster
   E* terms = reinterpret_cast<E*>(parts + kCluster * kR * 8);
-  __shared__ int s_tok[8], s_warp[kFewWarps];
+  __shared__ __align__(16) int s_adapter[kFewThreads];
+  __shared__ int s_first[kFewThreads], s_tok[8], s_warp[kFewWarps];
   __shared__ float s_up[8];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = lane >> 2, c = lane & 3;
   const int cta = static_cast<int>(sm100::cluster_ctarank());
-  const int64_t t = blockIdx.x / kCluster;
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
-  // (for up to as many tokens as threads, each looks at one adapter)
+  // The tokens of an adapter go in groups of eight in their order (those without an adapter as if
+  // they had one of their own).  For up to as many tokens as threads, a thread looks at one token
+  // and the clusters take the groups in turn; for more, the cluster of a group's first token takes
+  // it and the others leave.  (All CTAs of a cluster decide alike.)
   const bool one_look = p.tokens <= kFewThreads;
-  const int other = one_look && tid < p.tokens ? p.adapter[tid] : -1;
-  const int g = p.adapter[t];
-  const bool known = g >= 0 && g < p.n_adapters;
+  int64_t groups = p.tokens;
+  int mine = -2, before = 0;                               // the thread's token: its adapter, earlier tokens of it
+  if (one_look) {
+    if (tid < p.tokens) {
+      mine = p.adapter[tid];
+      if (mine < 0 || mine >= p.n_adapters) mine = -1;
+    }
+    s_adapter[tid] = mine;
+    __syncthreads();
+    if (warp * 32 < p.tokens)
+#pragma unroll 8
+      for (int i = 0; i < warp * 32; i += 4) {
+        const int4 q = *reinterpret_cast<const int4*>(s_adapter + i);
+        before += (q.x == mine) + (q.y == mine) + (q.z == mine) + (q.w == mine);
+      }
+    before += __popc(__match_any_sync(0xffffffffu, mine) & ((1u << lane) - 1));
+    const bool first = tid < p.tokens && before % 8 == 0;
+    const uint32_t m = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) s_warp[warp] = __popc(m);
+    __syncthreads();
+    int at = __popc(m & ((1u << lane) - 1)), all = 0;
+    for (int w = 0; w < kFewWarps; ++w) {
+      if (w < warp) at += s_warp[w];
+      all += s_warp[w];
+    }
+    if (first) s_first[at] = tid;
+    groups = all;
+  }
+  for (int64_t group = blockIdx.x / kCluster; group < groups; group += gridDim.x / kCluster) {
+  __syncthreads();                                         // the last group's s_tok has been read
+  const int64_t t = one_look ? s_first[group] : group;
+  int g = one_look ? s_adapter[t] : p.adapter[t];
+  if (g < 0 || g >= p.n_adapters) g = -1;
   int k = 0;
-  if (known) {
+  if (g >= 0) {
     k = p.ranks ? p.ranks[g] : p.rank;
     k = k < 0 ? 0 : k > p.rank ? p.rank : k;
   }
-  if (k == 0) {                                            // no adapter: y_in passes through
-    if (p.y != p.y_in) {
-      const float4* src = reinterpret_cast<const float4*>(p.y_in ? p.y_in + t * p.y_in_stride : nullptr);
-      float4* dst = reinterpret_cast<float4*>(p.y + t * p.y_stride);
-      for (int i = cta * kFewThreads + tid; i < p.d_out / 4; i += kCluster * kFewThreads)
-        dst[i] = src ? src[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    }
-    return;
-  }
-  // The tokens of an adapter go in groups of eight in their order; the cluster of a
-  // group's first token takes it, the others leave.  (All CTAs of a cluster decide alike.)
+  if (k == 0 && p.y == p.y_in) continue;
   if (tid < 8) s_tok[tid] = -1;
   if (one_look) {
-    const bool hit = other == g;
-    const uint32_t m = __ballot_sync(0xffffffffu, hit);
-    if (lane == 0) s_warp[warp] = m;
+    __shared__ int s_before;
+    if (tid == t) s_before = before;
     __syncthreads();
-    int before = 0, at = __popc(m & ((1u << lane) - 1));   // hits before t, and before this thread's
-    for (int w = 0; w < kFewWarps; ++w) {
-      const uint32_t q = s_warp[w];
-      if (w < static_cast<int>(t >> 5)) before += __popc(q);
-      else if (w == static_cast<int>(t >> 5)) before += __popc(q & ((1u << (t & 31)) - 1));
-      if (w < warp) at += __popc(q);
-    }
-    if (before % 8) return;
-    if (hit && at >= before && at < before + 8) s_tok[at - before] = tid;
+    if (mine == g && before >= s_before && before < s_before + 8) s_tok[before - s_before] = tid;
+    __syncthreads();
+  } else if (k == 0) {                                     // (each such token's own cluster)
+    if (tid == 0) s_tok[0] = static_cast<int>(t);
+    __syncthreads();
   } else {
-    int before = 0;
+    int earlier = 0;
     for (int64_t i0 = 0; i0 < t; i0 += kFewThreads) {
       const int64_t i = i0 + tid;
-      before += __syncthreads_count(i < t && p.adapter[i] == g);
+      earlier += __syncthreads_count(i < t && p.adapter[i] == g);
     }
-    if (before % 8) return;
+    if (earlier % 8) return;
     int found = 0;
     for (int64_t i0 = t; i0 < p.tokens && found < 8; i0 += kFewThreads) {
       const int64_t i = i0 + tid;
@@ -239,23 +262,45 @@ __global__ void __launch_bounds__(kFewThreads, MB <= 2 ? 3 : MB <= 8 ? 2 : 1)
       __syncthreads();
     }
   }
+  if (k == 0) {                                            // no adapter: y_in passes through, a warp for each token
+    if (s_tok[warp] >= 0) {
+      const float4* src = reinterpret_cast<const float4*>(p.y_in ? p.y_in + s_tok[warp] * p.y_in_stride : nullptr);
+      float4* dst = reinterpret_cast<float4*>(p.y + s_tok[warp] * p.y_stride);
+      for (int i0 = cta * 32 + lane; i0 < p.d_out / 4; i0 += kCluster * 32 * 4) {
+        float4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = i0 + j * kCluster * 32;
+          v[j] = src ? src[i < p.d_out / 4 ? i : i0] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i0 + j * kCluster * 32 < p.d_out / 4) dst[i0 + j * kCluster * 32] = v[j];
+      }
+    }
+    continue;
+  }
   // this CTA's blocks of 16 columns of y, and their rows of B
   const E* B = static_cast<const E*>(p.b) + static_cast<int64_t>(g) * p.d_out * p.rank;
   const int blocks = (p.d_out + 15) / 16, per = (blocks + kCluster - 1) / kCluster;
   const int nb_first = cta * per < blocks ? cta * per : blocks, nb_last = nb_first + per < blocks ? nb_first + per : blocks;
   const int n_last = nb_last * 16 < p.d_out ? nb_last * 16 : p.d_out;
-  cluster_arrive();                                        // this CTA runs: the others may write to it
-  prefetch_l2(B + static_cast<int64_t>(nb_first) * 16 * p.rank, static_cast<int64_t>(n_last - nb_first * 16) * p.rank * 2,
-              tid, kFewThreads);
+  // this CTA runs and has read its parts: the others may write to it (nothing is published yet)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  auto prefetch = [&] {                                    // of this CTA's part of B and of y_in into L2
+    prefetch_l2(B + static_cast<int64_t>(nb_first) * 16 * p.rank, static_cast<int64_t>(n_last - nb_first * 16) * p.rank * 2,
+                tid, kFewThreads);
+    if (p.y_in && s_tok[warp] >= 0 && nb_first < nb_last)
+      prefetch_l2(p.y_in + s_tok[warp] * p.y_in_stride + nb_first * 16, static_cast<int64_t>(n_last - nb_first * 16) * 4,
+                  lane, 32);
+  };
   __syncthreads();
-  if (p.y_in && s_tok[warp] >= 0 && nb_first < nb_last)
-    prefetch_l2(p.y_in + s_tok[warp] * p.y_in_stride + nb_first * 16, static_cast<int64_t>(n_last - nb_first * 16) * 4, lane, 32);
 
-  // s = A x, split over d_in between the 64 warps of the cluster
+  // s = A x, split over d_in between the warps of the cluster
   const E* A = static_cast<const E*>(p.a) + static_cast<int64_t>(g) * p.rank * p.d_in;
-  const int my_tok = s_tok[row];
-  const E* x = my_tok >= 0 ? static_cast<const E*>(p.x) + my_tok * p.x_stride : nullptr;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
+  // (Loads take no branch, so that all of a step's are in flight: columns of s without a token read
+  // the first one's x, rows from k on read row k - 1; neither is used.)
+  const E* x = static_cast<const E*>(p.x) + s_tok[s_tok[row] >= 0 ? row : 0] * p.x_stride;
   float acc[MB][4] = {};
   // (chains of 32 MMAs: see kChain; the warp's part is its lanes' own places)
   auto flush = [&](bool fresh) {
@@ -269,27 +314,38 @@ __global__ void __launch_bounds__(kFewThreads, MB <= 2 ? 3 : MB <= 8 ? 2 : 1)
     }
   };
   int steps = 0;
-  for (int kb = cta * kFewWarps + warp; kb < p.d_in / 32; kb += kCluster * kFewWarps, ++steps) {
+  constexpr int stride = kCluster * kFewWarps;
+  for (int kb = cta * kFewWarps + warp; kb < p.d_in / 32; kb += stride * kSteps, steps += kSteps) {
     if (steps && steps % 16 == 0) flush(steps == 16);
-    const int col = kb * 32 + c * 8;
-    const uint4 xv = x ? *reinterpret_cast<const uint4*>(x + col) : zero;
-    uint4 lo[MB], hi[MB];
+    uint4 xv[kSteps], lo[kSteps][MB], hi[kSteps][MB];
 #pragma unroll
-    for (int m = 0; m < MB; ++m) {
-      const int r0 = m * 16 + row, r1 = r0 + 8;
-      lo[m] = r0 < k ? *reinterpret_cast<const uint4*>(A + static_cast<int64_t>(r0) * p.d_in + col) : zero;
-      hi[m] = r1 < k ? *reinterpret_cast<const uint4*>(A + static_cast<int64_t>(r1) * p.d_in + col) : zero;
+    for (int j = 0; j < kSteps; ++j) {
+      const int col = (kb + j * stride < p.d_in / 32 ? kb + j * stride : kb) * 32 + c * 8;
+      xv[j] = *reinterpret_cast<const uint4*>(x + col);
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        const int r0 = m * 16 + row, r1 = r0 + 8;
+        lo[j][m] = *reinterpret_cast<const uint4*>(A + static_cast<int64_t>(r0 < k ? r0 : k - 1) * p.d_in + col);
+        hi[j][m] = *reinterpret_cast<const uint4*>(A + static_cast<int64_t>(r1 < k ? r1 : k - 1) * p.d_in + col);
+      }
     }
 #pragma unroll
-    for (int m = 0; m < MB; ++m) {
-      mma16816<E>(acc[m], lo[m].x, hi[m].x, lo[m].y, hi[m].y, xv.x, xv.y);
-      mma16816<E>(acc[m], lo[m].z, hi[m].z, lo[m].w, hi[m].w, xv.z, xv.w);
+    for (int j = 0; j < kSteps; ++j) {
+      if (j == 0 && steps == 0) prefetch();                // (behind the first loads of A, which are needed first)
+      if (kb + j * stride >= p.d_in / 32) break;
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        mma16816<E>(acc[m], lo[j][m].x, hi[j][m].x, lo[j][m].y, hi[j][m].y, xv[j].x, xv[j].y);
+        mma16816<E>(acc[m], lo[j][m].z, hi[j][m].z, lo[j][m].w, hi[j][m].w, xv[j].z, xv[j].w);
+      }
     }
   }
+  if (steps == 0) prefetch();
   flush(steps <= 16);
   __syncthreads();
   cluster_wait();
-  const int used = (k + 15) / 16 * 16 * 8;                 // of s, [rank][token]
+  constexpr int kPair = MB == 1 ? 1 : 2;                   // blocks of 16 ranks that a lane loads of B at once
+  const int used = (k + kPair * 16 - 1) / (kPair * 16) * (kPair * 16) * 8;    // of s, [rank][token]
   const uint32_t to = sm100::smem_u32(parts + cta * kR * 8);
   for (int i = tid * 4; i < used; i += kFewThreads * 4) {
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -299,11 +355,12 @@ __global__ void __launch_bounds__(kFewThreads, MB <= 2 ? 3 : MB <= 8 ? 2 : 1)
       s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
     }
 #pragma unroll
-    for (int r = 0; r < kCluster; ++r) st_cluster4(sm100::mapa_shared(to + i * 4, r), s);
+    for (int r = 0; r < kCluster; ++r)
+      st_cluster4(sm100::mapa_shared(to + i * 4, r), s);
   }
   cluster_arrive();
   cluster_wait();
-  // every CTA sums the eight CTAs' parts, in their order
+  // every CTA sums the CTAs' parts, in their order
   const float sc = p.scale ? p.scale[g] : 1.0f;
   float* total = part;                                     // [kR][8], the warps' parts are done with
   for (int i = tid * 4; i < used; i += kFewThreads * 4) {
@@ -313,6 +370,7 @@ __global__ void __launch_bounds__(kFewThreads, MB <= 2 ? 3 : MB <= 8 ? 2 : 1)
       const float4 q = *reinterpret_cast<const float4*>(parts + r * kR * 8 + i);
       s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
     }
+    if (i / 8 >= k) s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     *reinterpret_cast<float4*>(total + i) = make_float4(s.x * sc, s.y * sc, s.z * sc, s.w * sc);
   }
   __syncthreads();
@@ -337,54 +395,108 @@ __global__ void __launch_bounds__(kFewThreads, MB <= 2 ? 3 : MB <= 8 ? 2 : 1)
   __syncthreads();
 
   // y = y_in + B s
+  const bool is_half = std::is_same<E, __half>::value;
   const int tok0 = s_tok[c * 2], tok1 = s_tok[c * 2 + 1];
-  const float up0 = std::is_same<E, __half>::value ? s_up[c * 2] : 1.0f;
-  const float up1 = std::is_same<E, __half>::value ? s_up[c * 2 + 1] : 1.0f;
+  const float up0 = is_half ? s_up[c * 2] : 1.0f, up1 = is_half ? s_up[c * 2 + 1] : 1.0f;
+  // (no branches around loads here either: what is beyond this CTA's columns, the adapter's or a
+  // group's tokens reads some valid place)
+  const float* in0 = p.y_in ? p.y_in + (tok0 >= 0 ? tok0 : s_tok[0]) * p.y_in_stride : nullptr;
+  const float* in1 = p.y_in ? p.y_in + (tok1 >= 0 ? tok1 : s_tok[0]) * p.y_in_stride : nullptr;
+  float* out0 = tok0 >= 0 ? p.y + tok0 * p.y_stride : nullptr;
+  float* out1 = tok1 >= 0 ? p.y + tok1 * p.y_stride : nullptr;
+  // A lane's kPair x 8 consecutive bytes of a row of B are the k-places 2 c, 2 c + 1, 2 c + 8 and
+  // 2 c + 9 of kPair MMAs; the terms are read in the same order.
+  constexpr int kCols8 = kPair * 4;                        // columns of them
+  using Piece = typename std::conditional<kPair == 2, uint4, uint2>::type;
+  auto words = [](const Piece& v, int e, uint32_t* first, uint32_t* second) {
+    if constexpr (kPair == 2) {
+      *first = e ? v.z : v.x;
+      *second = e ? v.w : v.y;
+    } else {
+      *first = v.x;
+      *second = v.y;
+    }
+  };
+  auto term = [&](int m, int q) {
+    return *reinterpret_cast<const Piece*>(terms + (q * 8 + row) * kRow + m * kPair * 16 + c * kCols8);
+  };
+  constexpr int kM = MB / kPair;
+  constexpr bool kHeld = MB <= 4;                          // the terms stay in registers
+  Piece held[kHeld ? kM : 1][kT];
+  if constexpr (kHeld) {
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int q = 0; q < kT; ++q) held[m][q] = term(m, q);
+  }
   for (int nb = nb_first + warp * kUnroll; nb < nb_last; nb += kFewWarps * kUnroll) {
-    uint2 lo[kUnroll][MB], hi[kUnroll][MB];
+    Piece lo[kUnroll][kM], hi[kUnroll][kM];
     float old[kUnroll][4];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int n0 = (nb + u) * 16 + row, n1 = n0 + 8;
-      const bool in0 = nb + u < nb_last, in1 = in0 && n1 < p.d_out;      // (n0 < d_out: it is a multiple of 8)
+      const int n0 = (nb + u) * 16 + row, n1 = n0 + 8, at0 = n0 < n_last ? n0 : n_last - 1, at1 = n1 < n_last ? n1 : n_last - 1;
+      const E* b0 = B + static_cast<int64_t>(at0) * p.rank;
+      const E* b1 = B + static_cast<int64_t>(at1) * p.rank;
 #pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        const int col = m * 16 + c * 4;
-        lo[u][m] = hi[u][m] = make_uint2(0, 0);
-        if (in0 && col < k) lo[u][m] = *reinterpret_cast<const uint2*>(B + static_cast<int64_t>(n0) * p.rank + col);
-        if (in1 && col < k) hi[u][m] = *reinterpret_cast<const uint2*>(B + static_cast<int64_t>(n1) * p.rank + col);
+      for (int m = 0; m < kM; ++m) {
+        const int col = m * kPair * 16 + c * kCols8, from = col < p.rank ? col : 0;
+        lo[u][m] = *reinterpret_cast<const Piece*>(b0 + from);
+        hi[u][m] = *reinterpret_cast<const Piece*>(b1 + from);
       }
+      old[u][0] = old[u][1] = old[u][2] = old[u][3] = 0.0f;
+      if (p.y_in) {
+        old[u][0] = in0[at0];
+        old[u][1] = in1[at0];
+        old[u][2] = in0[at1];
+        old[u][3] = in1[at1];
+      }
+    }
+    if (k != kR) {                                         // columns from k on are padding that may hold anything
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int tok = j & 1 ? tok1 : tok0;
-        old[u][j] = p.y_in && tok >= 0 && (j < 2 ? in0 : in1) ? p.y_in[tok * p.y_in_stride + (j < 2 ? n0 : n1)] : 0.0f;
-      }
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int m = 0; m < kM; ++m) {
+          uint32_t* l = reinterpret_cast<uint32_t*>(&lo[u][m]);
+          uint32_t* h = reinterpret_cast<uint32_t*>(&hi[u][m]);
+#pragma unroll
+          for (int i = 0; i < kPair * 2; ++i) {
+            const int col = m * kPair * 16 + c * kCols8 + i * 2;
+            l[i] = keep_below(l[i], col, k);
+            h[i] = keep_below(h[i], col, k);
+          }
+        }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int n0 = (nb + u) * 16 + row, n1 = n0 + 8;
       float o[Split<E>::kSums][4] = {};
 #pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        const int col = m * 16 + c * 4;
-        if (m * 16 >= k) break;
-        // columns from k on are padding that may hold anything
-        const uint32_t a0 = keep_below(lo[u][m].x, col, k), a2 = keep_below(lo[u][m].y, col + 2, k);
-        const uint32_t a1 = keep_below(hi[u][m].x, col, k), a3 = keep_below(hi[u][m].y, col + 2, k);
+      for (int m = 0; m < kM; ++m) {
+        if (m * kPair * 16 >= k) break;
 #pragma unroll
         for (int q = 0; q < kT; ++q) {
-          const uint2 s = *reinterpret_cast<const uint2*>(terms + (q * 8 + row) * kRow + col);
-          mma16816<E>(o[q % Split<E>::kSums], a0, a1, a2, a3, s.x, s.y);
+          const Piece s = kHeld ? held[kHeld ? m : 0][q] : term(m, q);
+#pragma unroll
+          for (int e = 0; e < kPair; ++e) {
+            uint32_t a0, a1, a2, a3, s0, s1;
+            words(lo[u][m], e, &a0, &a2);
+            words(hi[u][m], e, &a1, &a3);
+            words(s, e, &s0, &s1);
+            mma16816<E>(o[q % Split<E>::kSums], a0, a1, a2, a3, s0, s1);
+          }
         }
       }
+      if (is_half) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = j < 2 ? n0 : n1, tok = j & 1 ? tok1 : tok0;
-        const float sum = std::is_same<E, __half>::value ? fmaf(o[Split<E>::kSums - 1][j], kDownSecond, o[0][j]) : o[0][j];
-        if (tok >= 0 && nb + u < nb_last && n < p.d_out)
-          p.y[tok * p.y_stride + n] = fmaf(sum, j & 1 ? up1 : up0, old[u][j]);
+        for (int j = 0; j < 4; ++j) o[0][j] = fmaf(o[Split<E>::kSums - 1][j], kDownSecond, o[0][j]);
       }
+      const bool has0 = n0 < n_last, has1 = n1 < n_last;
+      if (out0 && has0) out0[n0] = fmaf(o[0][0], up0, old[u][0]);
+      if (out1 && has0) out1[n0] = fmaf(o[0][1], up1, old[u][1]);
+      if (out0 && has1) out0[n1] = fmaf(o[0][2], up0, old[u][2]);
+      if (out1 && has1) out1[n1] = fmaf(o[0][3], up1, old[u][3]);
     }
+  }
   }
 }
 
@@ -393,12 +505,24 @@ int launch_few(const LoraArgs& p, cudaStream_t st) {
   constexpr int kR = MB * 16;
   constexpr int smem = (kFewWarps + kCluster) * kR * 8 * 4 + Split<E>::kTerms * 8 * (kR + 8) * 2;
   auto kern = lora_few_kernel<E, MB>;
-  if (smem > 48 * 1024 - 256) {
+  if (smem > 44 * 1024) {                                  // (and the kernel's own arrays)
     static std::atomic<uint64_t> done{0};
     if (set_smem_once(kern, smem, done) != WUSH_OK) return WUSH_ERR_CUDA;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.tokens * kCluster));
+  // As many clusters as lie on the GPU at once (each within one of its eight GPCs); those of up to
+  // kFewThreads tokens go on to further groups.  (200 tokens on 48 adapters, 4096 x 12288, rank
+  // 32: 21.4 us; a cluster a token, most of which leave at once: 26 us.)
+  int64_t clusters = p.tokens;
+  if (p.tokens > 16 && p.tokens <= kFewThreads) {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return WUSH_ERR_CUDA;
+    const int64_t most = sms / 8 * few_ctas(MB) / kCluster * 8;
+    if (clusters > most) clusters = most > 0 ? most : 1;
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * kCluster));
   cfg.blockDim = dim3(kFewThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -1286,11 +1410,10 @@ int launch_many(const LoraArgs& p, const Work& w, cudaStream_t st) {
   return launch_expand<E>(p, w, tiles, sms, st);
 }
 
-// Few tokens (or a pool too large to count in shared memory, or for a tensor map) go through
-// the cluster kernel, whose clusters each look through the adapters of all tokens.  Measured on
-// both sides: 200 tokens on 48 adapters, 4096 x 12288, rank 32: 31.1 us, 56 us by the three
-// launches; 276 tokens on one adapter, 352 x 4616, rank 128: 24.7 and 25.2 us; 391 tokens on one
-// adapter, 576 x 5296, rank 96: 37.6 and 23.0 us.
+// Few tokens (or a pool too large to count in shared memory, or for a tensor map) go through the
+// cluster kernel.  Measured on both sides, the cluster kernel first: 200 tokens on 48 adapters,
+// 4096 x 12288, rank 32: 21.4 and 57.2 us; 256 tokens on 12 adapters, 5120 x 4104, rank 48: 21.4
+// and 19.4; on 4, 12288 x 4096, rank 64: 18.5 and 23.2; on 2, 5120 x 17408, rank 16: 20.9 and 21.1.
 constexpr int kFewTokens = 256;
 
 constexpr int64_t kMostFewTokens = 4096;                   // a cluster's look through all tokens stays short
