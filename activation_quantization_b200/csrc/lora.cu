@@ -755,6 +755,14 @@ __device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// 16 rows of B in the order that expand's D wants (b_map): row 8 (the map's fourth axis) and on.
+__device__ __forceinline__ void tma_tile_b(uint32_t dst, const CUtensorMap* map, int col, int row8, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %4, %4, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(row8), "r"(0), "r"(sm100::smem_u32(bar))
+      : "memory");
+}
+
 // A wait that gives up sets the CTA's flag, and every later wait then gives up at once: the
 // roles run on to the CTA's common barriers, and the error is reported at the end.
 __device__ __forceinline__ void wait_or_flag(uint64_t* bar, uint32_t parity, int* abort_flag) {
@@ -1013,7 +1021,7 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __gri
 // The terms lie side by side in k, term t of rank j at k = t * row_elems + j, in operand tiles
 // of 64 (128-byte rows, 128-byte swizzle); each term's steps meet the same rows of B.  D comes
 // back in the layout of an m16n8 accumulator; of 16 columns, its block 0 is given those with
-// bit 1 clear and block 1 the others (TMA gathers B's rows in that order), so that a thread's
+// bit 1 clear and block 1 the others (TMA brings B's rows in that order), so that a thread's
 // values of both blocks are four consecutive columns: one 16-byte access of y each.
 //
 // One warp asks for the terms and B, one issues the MMAs, one draws pieces of work, eight add D
@@ -1152,19 +1160,16 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
         for (int i = 0; i < l.terms_bytes / (kTile * 128); ++i)
           tma_tile(s_base + i * (kTile * 128), &map_s, i * 64, q.tile.y, &s_full);
       }
-      // lane: rows of B in the order of D's columns, four at a time (16 groups for 64 columns)
-      const int group = lane & 15, n16 = (group >> 2) * 16 + ((group >> 1) & 1) * 2 + (group & 1) * 8;
+      const int row8 = static_cast<int>(static_cast<int64_t>(q.tile.x) * p.d_out / 8) + q.first * (kCols / 8);
       for (int b = 0; b < q.blocks; ++b, ++nb) {
-        const int s = nb % l.b_slots, n0 = (q.first + b) * kCols + n16;
+        const int s = nb % l.b_slots;
         wait_or_flag(&b_empty[s], ((nb / l.b_slots) & 1) ^ 1, &abort_flag);
         if (lane == 0) sm100::mbar_arrive_expect_tx(&b_full[s], units * kCols * 128);
         __syncwarp();
         // (columns beyond d_out read the next adapter's rows; their results are not stored)
-        const int64_t row = static_cast<int64_t>(q.tile.x) * p.d_out + n0;
-        const int4 rows = make_int4(static_cast<int>(row), static_cast<int>(row + 1), static_cast<int>(row + 4),
-                                    static_cast<int>(row + 5));
-        for (int u = lane >> 4; u < units; u += 2)
-          tma_gather4(b_ring + s * l.b_bytes + u * (kCols * 128) + group * 512, &map_b, u * 64, rows, &b_full[s]);
+        for (int i = lane; i < units * 4; i += 32)
+          tma_tile_b(b_ring + s * l.b_bytes + (i >> 2) * (kCols * 128) + (i & 3) * 2048, &map_b, (i >> 2) * 64,
+                     row8 + b * (kCols / 8) + (i & 3) * 2, &b_full[s]);
       }
     });
   } else if (warp == 9) {
@@ -1331,6 +1336,21 @@ bool tensor_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// B's rows [rows, rank] as n = 8 h + 4 c + 2 b + e, axes (column, e, c, h, b), in boxes of 64 columns x
+// 16 rows: rows with b = 0 first, so that D's blocks of eight columns hold those with bit 1 clear
+// and set in turn.
+template <typename E>
+bool b_map(CUtensorMap* map, const void* p, int64_t rows, int64_t rank) {
+  EncodeFn enc = get_encode();
+  const cuuint64_t r = static_cast<cuuint64_t>(rank), dims[5] = {r, 2, 2, static_cast<cuuint64_t>(rows / 8), 2};
+  const cuuint64_t strides[4] = {r * 2, r * 8, r * 16, r * 4};
+  const cuuint32_t box[5] = {64, 2, 2, 2, 2}, estr[5] = {1, 1, 1, 1, 1};
+  return enc && enc(map, std::is_same<E, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                    5, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename E, int R>
 int launch_shrink(const LoraArgs& p, const Work& w, int64_t tiles, int sms, cudaStream_t st) {
   constexpr int smem = Shrink<R>::kSmem;
@@ -1378,7 +1398,7 @@ int launch_expand(const LoraArgs& p, const Work& w, int64_t tiles, int sms, cuda
   const int64_t slots = int64_t(sms) * (l.smem <= kMaxSmem / 2 ? 2 : 1);
   CUtensorMap map_s, map_b;
   if (!tensor_map<E>(&map_s, w.terms, p.tokens, Split<E>::kTerms * w.row_elems, Split<E>::kTerms * w.row_elems, kTile) ||
-      !tensor_map<E>(&map_b, p.b, int64_t(p.n_adapters) * p.d_out, p.rank, p.rank, 1))
+      !b_map<E>(&map_b, p.b, int64_t(p.n_adapters) * p.d_out, p.rank))
     return WUSH_ERR_CUDA;
   return launch_pdl(kern, static_cast<unsigned>(items < slots ? items : slots), kExpandThreads, l.smem, st, p, w, l, map_s,
                     map_b);
