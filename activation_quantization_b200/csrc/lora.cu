@@ -1115,6 +1115,13 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
     int first, blocks;
   };
   int turn = 0;
+  struct Slot {                                            // of a ring, and the parity of its turn
+    int i;
+    uint32_t turn;
+    __device__ __forceinline__ void next(int slots) {
+      if (++i == slots) i = 0, turn ^= 1;
+    }
+  };
   // Calls f for each stretch of a piece within one tile, piece after piece, until none is left.
   auto for_pieces = [&](auto f) __attribute__((always_inline)) {
     for (;; ++turn) {
@@ -1126,8 +1133,9 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
       const int64_t to = pos + size < all ? pos + size : all;
       while (pos < to) {
         Piece q;
-        q.tile = w.tiles[pos / blocks];
-        q.first = static_cast<int>(pos % blocks);
+        const int64_t tile = all >> 32 ? pos / blocks : static_cast<uint32_t>(pos) / static_cast<uint32_t>(blocks);
+        q.tile = w.tiles[tile];
+        q.first = static_cast<int>(pos - tile * blocks);
         q.blocks = to - pos < blocks - q.first ? static_cast<int>(to - pos) : blocks - q.first;
         f(q);
         pos += q.blocks;
@@ -1149,7 +1157,8 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
     __syncwarp();
   } else
   if (warp == 8) {
-    int nb = 0, ns = 0;                                    // blocks of B and tiles' terms asked for so far
+    int ns = 0;                                            // tiles' terms asked for so far
+    Slot slot = {0, 1};                                    // of B
     for_pieces([&](const Piece& q) {
       const int k = q.tile.w, units = (k + 63) / 64;
       if (k == 0) return;
@@ -1161,9 +1170,9 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
           tma_tile(s_base + i * (kTile * 128), &map_s, i * 64, q.tile.y, &s_full);
       }
       const int row8 = static_cast<int>(static_cast<int64_t>(q.tile.x) * p.d_out / 8) + q.first * (kCols / 8);
-      for (int b = 0; b < q.blocks; ++b, ++nb) {
-        const int s = nb % l.b_slots;
-        wait_or_flag(&b_empty[s], ((nb / l.b_slots) & 1) ^ 1, &abort_flag);
+      for (int b = 0; b < q.blocks; ++b, slot.next(l.b_slots)) {
+        const int s = slot.i;
+        wait_or_flag(&b_empty[s], slot.turn, &abort_flag);
         if (lane == 0) sm100::mbar_arrive_expect_tx(&b_full[s], units * kCols * 128);
         __syncwarp();
         // (columns beyond d_out read the next adapter's rows; their results are not stored)
@@ -1174,16 +1183,17 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
     });
   } else if (warp == 9) {
     int nb = 0, ns = 0;
+    Slot slot = {0, 0};
     constexpr uint32_t idesc = idesc_f16_m64<E>(kCols);
     for_pieces([&](const Piece& q) {
       const int k = q.tile.w, kp = (k + 15) / 16 * 16;
       if (k == 0) return;
       wait_or_flag(&s_full, ns & 1, &abort_flag);
       ++ns;
-      for (int b = 0; b < q.blocks; ++b, ++nb) {
-        const int s = nb % l.b_slots, d = nb & 1;
+      for (int b = 0; b < q.blocks; ++b, ++nb, slot.next(l.b_slots)) {
+        const int s = slot.i, d = nb & 1;
         const uint32_t at = b_ring + s * l.b_bytes;
-        wait_or_flag(&b_full[s], (nb / l.b_slots) & 1, &abort_flag);
+        wait_or_flag(&b_full[s], slot.turn, &abort_flag);
         if (k < kp) {
           // columns from k on are padding that may hold anything: the last step's become zero
           for (int r = lane; r < kCols; r += 32)
@@ -1224,9 +1234,11 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
       const float* src1 = p.y_in ? p.y_in + t1 * p.y_in_stride + col : nullptr;
       float* dst0 = p.y + t0 * p.y_stride + col;
       float* dst1 = p.y + t1 * p.y_stride + col;
+      const bool some = wm * 16 < count;                   // of the warp's rows
+      int to = 0, from = 0;                                // slots: the next to fill, to read
       auto fetch = [&](int b) {
-        if (p.y_in && b < q.blocks) {
-          const uint32_t slot = y_ring + b % l.y_slots * kSlot + tid * 16;
+        if (p.y_in && some && b < q.blocks) {
+          const uint32_t slot = y_ring + to * kSlot + tid * 16;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int n = b * kCols + j * 16;
@@ -1236,6 +1248,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
           }
         }
         cp_async_commit();
+        to = to + 1 == l.y_slots ? 0 : to + 1;
       };
       float up0 = 1.0f, up1 = 1.0f;
       if (std::is_same<E, __half>::value && k) {
@@ -1253,7 +1266,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
           const int d = nb & 1;
           wait_or_flag(&d_full[d], (nb >> 1) & 1, &abort_flag);
           ++nb;
-          if (wm * 16 < count) {
+          if (some) {
             sm100::tc_fence_after();
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -1276,7 +1289,9 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
           __syncwarp();
           if (lane == 0) sm100::mbar_arrive(&d_empty[d]);
         }
-        const float4* slots = reinterpret_cast<const float4*>(smem + (y_ring - s_base) + b % l.y_slots * kSlot) + tid;
+        const float4* slots = reinterpret_cast<const float4*>(smem + (y_ring - s_base) + from * kSlot) + tid;
+        from = from + 1 == l.y_slots ? 0 : from + 1;
+        if (!some) continue;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int n = b * kCols + j * 16;
