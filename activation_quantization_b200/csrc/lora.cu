@@ -135,6 +135,7 @@ __device__ __forceinline__ uint32_t keep_below(uint32_t pair, int col, int k) { 
 // as both operands share it, so a lane takes 16 consecutive bytes of a row of A, 8 of B).
 // ---------------------------------------------------------------------------
 constexpr int kCluster = 8, kFewThreads = 256, kFewWarps = kFewThreads / 32;
+constexpr int kLooks = 2, kLookTokens = kLooks * kFewThreads;      // tokens that the threads of a CTA look at together
 
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   float v;
@@ -165,9 +166,9 @@ __device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v) {
 // are in flight before any is used.  B and y_in are on their way into L2 while s is computed, a
 // warp asks for several blocks of B (kUnroll) before it multiplies any, and a CTA writes its sums
 // to the others before they meet, so that nobody reads across after it.  1 token, 4096 x 4096,
-// rank 16: 4.1 us, of which about 0.5 go to the adapter's number, 0.5 to the grouping, 0.6 to A,
+// rank 16: 4.4 us, of which about 0.5 go to the adapter's number, 0.5 to the grouping, 0.6 to A,
 // 1.2 to the sums and terms, 0.9 to B and y.  16 tokens, 4096 x 4096, rank 64, one adapter each:
-// 8.9 us, 2.1 TB/s; 48 of rank 32, 4096 x 12288: 18.0 us, 3.1 TB/s.
+// 9.3 us, 1.9 TB/s; 200 on 48 adapters of rank 32, 4096 x 12288: 22.0 us, 3.3 TB/s.
 constexpr int few_ctas(int mb) { return mb <= 2 ? 3 : mb <= 8 ? 2 : 1; }   // an SM
 
 template <typename E, int MB>
@@ -179,8 +180,8 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(MB))
   float* part = reinterpret_cast<float*>(smem);
   float* parts = part + kFewWarps * kR * 8;                // written by the CTAs of the cluster
   E* terms = reinterpret_cast<E*>(parts + kCluster * kR * 8);
-  __shared__ __align__(16) int s_adapter[kFewThreads];
-  __shared__ int s_first[kFewThreads], s_tok[8], s_warp[kFewWarps];
+  __shared__ __align__(16) int s_adapter[kLookTokens];
+  __shared__ int s_first[kLookTokens], s_tok[8], s_warp[kLooks * kFewWarps], s_before;
   __shared__ float s_up[8];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = lane >> 2, c = lane & 3;
@@ -188,36 +189,54 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(MB))
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
   // The tokens of an adapter go in groups of eight in their order (those without an adapter as if
-  // they had one of their own).  For up to as many tokens as threads, a thread looks at one token
-  // and the clusters take the groups in turn; for more, the cluster of a group's first token takes
-  // it and the others leave.  (All CTAs of a cluster decide alike.)
-  const bool one_look = p.tokens <= kFewThreads;
+  // they had one of their own).  Up to kLookTokens, a thread looks at one or two tokens and the
+  // clusters take the groups in turn; for more, the cluster of a group's first token takes it and
+  // the others leave.  (All CTAs of a cluster decide alike.)
+  const bool one_look = p.tokens <= kLookTokens;
   int64_t groups = p.tokens;
-  int mine = -2, before = 0;                               // the thread's token: its adapter, earlier tokens of it
+  int mine[kLooks] = {-2, -2}, before[kLooks] = {};        // the thread's tokens: their adapters, earlier tokens of these
   if (one_look) {
-    if (tid < p.tokens) {
-      mine = p.adapter[tid];
-      if (mine < 0 || mine >= p.n_adapters) mine = -1;
-    }
-    s_adapter[tid] = mine;
-    __syncthreads();
-    if (warp * 32 < p.tokens)
-#pragma unroll 8
-      for (int i = 0; i < warp * 32; i += 4) {
-        const int4 q = *reinterpret_cast<const int4*>(s_adapter + i);
-        before += (q.x == mine) + (q.y == mine) + (q.z == mine) + (q.w == mine);
+    const int tokens = static_cast<int>(p.tokens);
+#pragma unroll
+    for (int j = 0; j < kLooks; ++j) {
+      if (j * kFewThreads >= tokens) break;
+      const int i = j * kFewThreads + tid;
+      if (i < tokens) {
+        mine[j] = p.adapter[i];
+        if (mine[j] < 0 || mine[j] >= p.n_adapters) mine[j] = -1;
       }
-    before += __popc(__match_any_sync(0xffffffffu, mine) & ((1u << lane) - 1));
-    const bool first = tid < p.tokens && before % 8 == 0;
-    const uint32_t m = __ballot_sync(0xffffffffu, first);
-    if (lane == 0) s_warp[warp] = __popc(m);
-    __syncthreads();
-    int at = __popc(m & ((1u << lane) - 1)), all = 0;
-    for (int w = 0; w < kFewWarps; ++w) {
-      if (w < warp) at += s_warp[w];
-      all += s_warp[w];
+      s_adapter[i] = mine[j];
     }
-    if (first) s_first[at] = tid;
+    __syncthreads();
+    bool first[kLooks] = {};
+#pragma unroll
+    for (int j = 0; j < kLooks; ++j) {
+      if (j * kFewThreads >= tokens) break;
+      const int i0 = j * kFewThreads + warp * 32;          // of the warp's tokens
+      if (i0 < tokens) {
+#pragma unroll 8
+        for (int i = 0; i < i0; i += 4) {
+          const int4 q = *reinterpret_cast<const int4*>(s_adapter + i);
+          before[j] += (q.x == mine[j]) + (q.y == mine[j]) + (q.z == mine[j]) + (q.w == mine[j]);
+        }
+        before[j] += __popc(__match_any_sync(0xffffffffu, mine[j]) & ((1u << lane) - 1));
+      }
+      first[j] = i0 + lane < tokens && before[j] % 8 == 0;
+      const uint32_t m = __ballot_sync(0xffffffffu, first[j]);
+      if (lane == 0) s_warp[j * kFewWarps + warp] = __popc(m);
+    }
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int j = 0; j < kLooks; ++j) {
+      if (j * kFewThreads >= tokens) break;
+      int at = all + __popc(__ballot_sync(0xffffffffu, first[j]) & ((1u << lane) - 1));
+      for (int w = 0; w < kFewWarps; ++w) {
+        if (w < warp) at += s_warp[j * kFewWarps + w];
+        all += s_warp[j * kFewWarps + w];
+      }
+      if (first[j]) s_first[at] = j * kFewThreads + tid;
+    }
     groups = all;
   }
   for (int64_t group = blockIdx.x / kCluster; group < groups; group += gridDim.x / kCluster) {
@@ -233,10 +252,13 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(MB))
   if (k == 0 && p.y == p.y_in) continue;
   if (tid < 8) s_tok[tid] = -1;
   if (one_look) {
-    __shared__ int s_before;
-    if (tid == t) s_before = before;
+#pragma unroll
+    for (int j = 0; j < kLooks; ++j)
+      if (j * kFewThreads + tid == t) s_before = before[j];
     __syncthreads();
-    if (mine == g && before >= s_before && before < s_before + 8) s_tok[before - s_before] = tid;
+#pragma unroll
+    for (int j = 0; j < kLooks; ++j)
+      if (mine[j] == g && before[j] >= s_before && before[j] < s_before + 8) s_tok[before[j] - s_before] = j * kFewThreads + tid;
     __syncthreads();
   } else if (k == 0) {                                     // (each such token's own cluster)
     if (tid == 0) s_tok[0] = static_cast<int>(t);
@@ -505,16 +527,16 @@ int launch_few(const LoraArgs& p, cudaStream_t st) {
   constexpr int kR = MB * 16;
   constexpr int smem = (kFewWarps + kCluster) * kR * 8 * 4 + Split<E>::kTerms * 8 * (kR + 8) * 2;
   auto kern = lora_few_kernel<E, MB>;
-  if (smem > 44 * 1024) {                                  // (and the kernel's own arrays)
+  if (smem > 40 * 1024) {                                  // (and the kernel's own arrays)
     static std::atomic<uint64_t> done{0};
     if (set_smem_once(kern, smem, done) != WUSH_OK) return WUSH_ERR_CUDA;
   }
   cudaLaunchConfig_t cfg = {};
   // As many clusters as lie on the GPU at once (each within one of its eight GPCs); those of up to
-  // kFewThreads tokens go on to further groups.  (200 tokens on 48 adapters, 4096 x 12288, rank
-  // 32: 21.4 us; a cluster a token, most of which leave at once: 26 us.)
+  // kLookTokens tokens go on to further groups.  (200 tokens on 48 adapters, 4096 x 12288, rank
+  // 32: 21.4 us; a cluster a token, most of which leave at once: some 5 us more.)
   int64_t clusters = p.tokens;
-  if (p.tokens > 16 && p.tokens <= kFewThreads) {
+  if (p.tokens > 16 && p.tokens <= kLookTokens) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -1446,15 +1468,19 @@ int launch_many(const LoraArgs& p, const Work& w, cudaStream_t st) {
 }
 
 // Few tokens (or a pool too large to count in shared memory, or for a tensor map) go through the
-// cluster kernel.  Measured on both sides, the cluster kernel first: 200 tokens on 48 adapters,
-// 4096 x 12288, rank 32: 21.4 and 57.2 us; 256 tokens on 12 adapters, 5120 x 4104, rank 48: 21.4
-// and 19.4; on 4, 12288 x 4096, rank 64: 18.5 and 23.2; on 2, 5120 x 17408, rank 16: 20.9 and 21.1.
+// cluster kernel: up to 256, or up to 512 where the pool may hold an adapter for every eight of
+// them.  Measured on both sides, the cluster kernel first: 256 tokens on 48 adapters, 4096 x 12288,
+// rank 32: 22.9 and 48.3 us; on 12, 5120 x 4104, rank 48: 21.2 and 18.5; on 4, 12288 x 4096, rank 64:
+// 18.2 and 23.1.  512 tokens, 4096 x 4096, on 64 adapters of rank 64: 35.6 and 45.4; on 256 of rank
+// 16: 40.3 and 76.2; all on one of 64, rank 64: 36.3 and 20.0; on 4 of 4, 12288 x 4096: 42.9 and 26.5.
 constexpr int kFewTokens = 256;
 
 constexpr int64_t kMostFewTokens = 4096;                   // a cluster's look through all tokens stays short
 
 bool large_pool(int64_t n, int64_t d_out) { return n > kPlanAdapters || n * d_out > 0x7fffffff; }
-bool few(int64_t tokens, int64_t n, int64_t d_out) { return tokens <= kFewTokens || large_pool(n, d_out); }
+bool few(int64_t tokens, int64_t n, int64_t d_out) {
+  return tokens <= kFewTokens || (tokens <= kLookTokens && n >= tokens / 8) || large_pool(n, d_out);
+}
 
 template <typename E>
 int run_lora(const LoraArgs& p, void* workspace, cudaStream_t st) {

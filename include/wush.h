@@ -525,14 +525,15 @@ int wush_norm(const void* x, int x_dtype, int64_t x_stride, int64_t rows, int64_
  * y:        device fp32 [tokens, d_out], row stride a multiple of 4; may be y_in (with
  *           its stride), otherwise it may overlap neither y_in nor x.
  * workspace: device, at least wush_lora_workspace_bytes(...) bytes, 16-byte aligned, apart
- *           from x, y_in and y; may be NULL where that is 0 (256 tokens or fewer).  Calls
+ *           from x, y_in and y; may be NULL where that is 0 (256 tokens or fewer, and
+ *           up to 512 of pools with an adapter for every eight tokens).  Calls
  *           that can overlap in time (two streams, two graphs) need one each.  What it
  *           holds before and after a call is of no meaning.
  * Requirements: 0 <= tokens <= 2^24 (0: nothing is launched), d_in % 32 == 0,
  * d_out % 8 == 0, both <= 2^24, rank % 8 == 0, 8 <= rank <= 256, n_adapters <= 2^20; with
  * n_adapters > 57344 or n_adapters * d_out >= 2^31, tokens <= 4096.
- * WUSH_ERR_BUFFER_TOO_SMALL for a small workspace.  Up to 256 tokens take one launch, more
- * take three. */
+ * WUSH_ERR_BUFFER_TOO_SMALL for a small workspace.  Calls without a workspace take one
+ * launch, the others three. */
 typedef struct {
   const void* x;
   const int32_t* adapter;

@@ -273,3 +273,14 @@ def test_small_ranks_beside_large_ones(lib, tokens, dt):
     want = (x.double() @ a[0].double().T) @ b[0].double().T
     err = (y.double() - want).abs()
     assert bool((err <= 80 * 2 * U * want).all()), float((err / want).max())
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("tokens", [256, 257, 300, 511, 512, 513])
+def test_two_tokens_a_thread(lib, tokens, dt):
+    # pools with an adapter for every eight tokens stay in one launch up to 512 tokens
+    assert (lib.wush_lora_workspace_bytes(tokens, 256, 136, 70, 24) == 0) == (tokens <= 512)
+    t = torch.arange(tokens)
+    for ad in (torch.full((tokens,), 69), t % 70, t * 7 // tokens, torch.where(t % 3 == 0, -1, t % 64)):
+        check(lib, tokens, 256, 136, 70, 24, dt, adapter=ad)
+    check(lib, tokens, 256, 136, 70, 24, dt, adapter=torch.where(t % 3 == 0, -1, t % 64), in_place=True)
