@@ -310,27 +310,25 @@ __global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __
     return Bounds{(at + 15) & ~int64_t(15),
                   reinterpret_cast<int64_t>(row_of(p, dt, (a.rows - 1) * stride + d)) & ~int64_t(15)};
   };
-  auto units = [&](int64_t at, int size, const Bounds& m, int64_t* lo) {
+  struct Units {
+    int64_t lo;
+    uint32_t bytes;
+  };
+  auto units = [&](int64_t at, int size, const Bounds& m) {
     const int64_t end = at + int64_t(d) * size;
-    if (MODE == kAligned) {
-      *lo = at;
-      return static_cast<uint32_t>(end - at);
-    }
+    if (MODE == kAligned) return Units{at, static_cast<uint32_t>(end - at)};
     const int64_t from = at & ~int64_t(15), to = (end + 15) & ~int64_t(15), hi = to < m.hi ? to : m.hi;
-    *lo = from > m.lo ? from : m.lo;
-    return hi > *lo ? static_cast<uint32_t>(hi - *lo) : 0u;
+    const int64_t lo = from > m.lo ? from : m.lo;
+    return Units{lo, hi > lo ? static_cast<uint32_t>(hi - lo) : 0u};
   };
-  auto bulk = [&](int64_t at, int size, const Bounds& m, char* to, uint64_t* bar) {
-    int64_t lo;
-    const uint32_t bytes = units(at, size, m, &lo);
-    if (bytes) sm100::bulk_load(to + (at & 15) + (lo - at), reinterpret_cast<const void*>(lo), bytes, bar);
+  auto bulk = [&](int64_t at, const Units& u, char* to, uint64_t* bar) {
+    if (u.bytes) sm100::bulk_load(to + (at & 15) + (u.lo - at), reinterpret_cast<const void*>(u.lo), u.bytes, bar);
   };
-  auto ends = [&](int64_t at, int size, const Bounds& m, char* to) {
-    int64_t lo;
-    const uint32_t bytes = units(at, size, m, &lo);
-    const int64_t hi = lo + bytes, end = at + int64_t(d) * size;
-    const int head = !bytes ? d : lo > at ? static_cast<int>(lo - at) / size : 0;       // elements before the units
-    const int tail = !bytes ? d : hi < end ? static_cast<int>(hi - at) / size : d;      // first element behind them
+  auto ends = [&](int64_t at, int size, const Units& u, char* to) {
+    const int64_t hi = u.lo + u.bytes, end = at + int64_t(d) * size;
+    if (u.bytes && u.lo <= at && hi >= end) return;
+    const int head = !u.bytes ? d : u.lo > at ? static_cast<int>(u.lo - at) / size : 0;   // elements before the units
+    const int tail = !u.bytes ? d : hi < end ? static_cast<int>(hi - at) / size : d;      // first element behind them
     for (int i = tid; i < head + (d - tail); i += 32) {
       const int e = (i < head ? i : tail + i - head) * size;
       char* dst = to + (at & 15) + e;
@@ -350,12 +348,12 @@ __global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __
     if (!a.y || i >= n_rows || tid >= (MODE == kAligned ? 1 : 32)) return;
     const int64_t at = address(a.y, a.y_dt, a.y_stride, i);
     char* to = smem + q.y + s * q.y_step;
+    const Units u = units(at, y_size, in_y);
     if (tid == 0) {
-      int64_t lo;
-      sm100::mbar_arrive_expect_tx(&full[0][s], units(at, y_size, in_y, &lo));
-      bulk(at, y_size, in_y, to, &full[0][s]);
+      sm100::mbar_arrive_expect_tx(&full[0][s], u.bytes);
+      bulk(at, u, to, &full[0][s]);
     }
-    if (MODE != kAligned) ends(at, y_size, in_y, to);
+    if (MODE != kAligned) ends(at, y_size, u, to);
   };
   auto fill_rest = [&](int i, int s) {
     if (i >= n_rows || tid >= (MODE == kAligned ? 1 : 32)) return;
@@ -363,15 +361,14 @@ __global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __
     const int64_t at_g = gate_ring ? address(a.gate, a.gate_dt, a.gate_stride, i) : 0;
     char* to_r = smem + q.r + s * q.r_step;
     char* to_g = smem + q.gate + s * q.gate_step;
+    const Units u_r = r_ring ? units(at_r, r_size, in_r) : Units{0, 0}, u_g = gate_ring ? units(at_g, gate_size, in_g) : Units{0, 0};
     if (tid == 0) {
-      int64_t lo;
-      sm100::mbar_arrive_expect_tx(&full[1][s], (r_ring ? units(at_r, r_size, in_r, &lo) : 0u) +
-                                                    (gate_ring ? units(at_g, gate_size, in_g, &lo) : 0u));
-      if (r_ring) bulk(at_r, r_size, in_r, to_r, &full[1][s]);
-      if (gate_ring) bulk(at_g, gate_size, in_g, to_g, &full[1][s]);
+      sm100::mbar_arrive_expect_tx(&full[1][s], u_r.bytes + u_g.bytes);
+      if (r_ring) bulk(at_r, u_r, to_r, &full[1][s]);
+      if (gate_ring) bulk(at_g, u_g, to_g, &full[1][s]);
     }
-    if (MODE != kAligned && r_ring) ends(at_r, r_size, in_r, to_r);
-    if (MODE != kAligned && gate_ring) ends(at_g, gate_size, in_g, to_g);
+    if (MODE != kAligned && r_ring) ends(at_r, r_size, u_r, to_r);
+    if (MODE != kAligned && gate_ring) ends(at_g, gate_size, u_g, to_g);
   };
   // (a wait that gives up marks the error and lets the CTA run on, so that its barriers
   // stay uniform; every later wait then gives up at once)
@@ -387,8 +384,11 @@ __global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __
     fill_y(i, i);
     fill_rest(i, i);
   }
-  // Meanwhile the vectors that every row uses, as fp32 and shifted like the rows; all of a
-  // thread's elements of all vectors are asked for before any is stored.
+  // Meanwhile the vectors that every row uses, as fp32 and shifted like the rows; eight elements of
+  // each are asked for before any is stored.  (Where rows are shifted a vector is not, and its
+  // elements go to the threads one by one, so that a warp's lie side by side on both sides.)
+  constexpr int kVecMode = MODE == kAligned ? kAligned : kScalar;
+  const Columns<kVecMode> flat = {g, tid, d, 0, false};
   Vectors post = {q.kept, nullptr, nullptr}, pre = post;
   const float* gate_vec = nullptr;
   if (q.kept) {
@@ -406,14 +406,14 @@ __global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __
         with_dtype(src[2] || src[3] || src[4] ? src[4] ? dts[4] : dts[2] : dts[0], [&](auto t) __attribute__((always_inline)) {
 #pragma unroll
           for (int n = 0; n < 5; ++n)
-            if (src[n]) load_group<t.value, MODE, true>(src[n], j, cols, x[n]);
+            if (src[n]) load_group<t.value, kVecMode, true>(src[n], j, flat, x[n]);
         });
       } else {
 #pragma unroll
         for (int n = 0; n < 5; ++n)
           if (src[n])
             with_dtype(dts[n], [&](auto t) __attribute__((always_inline)) {
-              load_group<t.value, MODE, true>(src[n], j, cols, x[n]);
+              load_group<t.value, kVecMode, true>(src[n], j, flat, x[n]);
             });
       }
 #pragma unroll
@@ -421,8 +421,8 @@ __global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __
         if (src[n])
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int c = cols.at(j, e);
-            if (cols.has(c)) dst[n][c] = x[n][e] + offset[n];
+            const int c = flat.at(j, e);
+            if (flat.has(c)) dst[n][c] = x[n][e] + offset[n];
           }
     }
     post.w = dst[0]; post.b = dst[1];
@@ -570,6 +570,7 @@ template <int MODE>
 int launch_width(const Args& a, int sms, cudaStream_t st) {
   const int d = a.d + (MODE == kShifted ? 3 : 0);
   if (d <= 4096) return launch_ring<MODE, 2, 256>(a, sms, st);
+  if (d <= 5120) return launch_ring<MODE, 2, 320>(a, sms, st);
   if (d <= 6144) return launch_ring<MODE, 3, 256>(a, sms, st);
   if (d <= 8192) return launch_ring<MODE, 4, 256>(a, sms, st);
   if (d <= 12288) return launch_ring<MODE, 3, 512>(a, sms, st);
