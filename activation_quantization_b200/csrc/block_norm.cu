@@ -15,10 +15,11 @@
 //    registers (latency counts);
 //  * many rows: persistent CTAs, each with a ring of whole rows in shared memory that
 //    bulk copies fill ahead of it, so that the bytes in flight do not depend on how
-//    many threads wait.  4096 rows x 4096, fp32 y, bf16 stream and h: 29.0 us, 5.79 TB/s;
-//    8192 x 5120 bf16, the norm alone: 30.3 us, 5.54 TB/s; 2048 x 12288 fp32 with layer
-//    norms and a gate per element: 92 us, 4.93 TB/s (its four vectors do not fit beside
-//    the rows and are read from L2 for each row).
+//    many threads wait.  4096 rows x 4096, fp32 y, bf16 stream and h: 28.9 us, 5.81 TB/s;
+//    8192 x 5120 bf16, the norm alone: 30.1 us, 5.57 TB/s; 2048 x 12288 fp32 with layer
+//    norms and a gate per element: 91 us, 4.96 TB/s (its four vectors do not fit beside
+//    the rows and are read from L2 for each row); 1531 x 4097 bf16 with a gate per element, rows
+//    at any element: 23.3 us, 2.70 TB/s (three rows a CTA, about 9000 cycles each).
 #include "rowops.cuh"
 #include "sm100.cuh"
 
@@ -154,7 +155,7 @@ __device__ __forceinline__ void apply_norm(const Args& a, const NormArgs& n, con
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float x[8];
-        load_group<dt.value, MODE, true>(n.w, j, q, x);
+        load_group<dt.value, MODE>(n.w, j, q, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] += n.offset;
         scale8(v[j], f);
@@ -177,7 +178,7 @@ __device__ __forceinline__ void apply_norm(const Args& a, const NormArgs& n, con
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float x[8];
-        load_group<dt.value, MODE, true>(n.b, j, q, x);
+        load_group<dt.value, MODE>(n.b, j, q, x);
         add8(v[j], x);
       }
     });
@@ -283,14 +284,15 @@ __global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __
   Columns<MODE> cols = {g, tid, d, MODE == kShifted ? (a.phase + static_cast<int>(blockIdx.x & 3) * a.phase_step) & 3 : 0,
                         false};
   if (MODE == kShifted) cols.edges = cols.find_edges(NV);
-  const bool gate_rows = a.gate && a.gate_stride;
+  const bool gate_rows = a.gate && a.gate_stride, gate_ring = gate_rows && q.gate >= 0, r_ring = a.r && q.r >= 0;
+  const int lane = tid & 31;
   const int n_rows = static_cast<int>((a.rows - 1 - blockIdx.x) / gridDim.x) + 1;   // (at most one CTA a row)
 
   if (tid == 0) {
     abort_flag = 0;
     for (int i = 0; i < q.stages; ++i) {
       mbar_init(&full[0][i], 1);
-      mbar_init(&full[1][i], 1);
+      mbar_init(&full[1][i], gate_ring ? 2 : 1);
     }
     sm100::fence_barrier_init();
   }
@@ -298,10 +300,11 @@ __global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __
   sm100::pdl_wait();                                       // nothing global is touched before this
   sm100::pdl_launch_dependents();
   __syncthreads();                                         // the barriers are set up
-  // One row of one tensor into its stage, by a bulk copy (thread 0) of the 16-byte units that
-  // it touches: ``units`` gives their first byte and their number of bytes.  What a unit holds
+  // One row of one tensor into its stage, by a bulk copy of the 16-byte units that it touches:
+  // ``units`` gives their first byte and their number of bytes.  Each tensor has a warp for it (y
+  // the third, r the first, the gate the second), since the slowest warp holds up the row.  What a unit holds
   // beside the row is never used.  Units that reach beyond the matrix (its first row's first,
-  // its last row's last) are left out, and the first warp copies the elements there.
+  // its last row's last) are left out, and the warp copies the elements there.
   struct Bounds {
     int64_t lo, hi;                                        // the matrix's whole units
   };
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __
     if (u.bytes && u.lo <= at && hi >= end) return;
     const int head = !u.bytes ? d : u.lo > at ? static_cast<int>(u.lo - at) / size : 0;   // elements before the units
     const int tail = !u.bytes ? d : hi < end ? static_cast<int>(hi - at) / size : d;      // first element behind them
-    for (int i = tid; i < head + (d - tail); i += 32) {
+    for (int i = lane; i < head + (d - tail); i += 32) {
       const int e = (i < head ? i : tail + i - head) * size;
       char* dst = to + (at & 15) + e;
       if (size == 4) *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(at + e);
@@ -341,34 +344,29 @@ __global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __
   auto address = [&](const void* p, int dt, int64_t stride, int i) {       // of the CTA's row i
     return reinterpret_cast<int64_t>(row_of(p, dt, (blockIdx.x + int64_t(i) * gridDim.x) * stride));
   };
-  const bool r_ring = a.r && q.r >= 0, gate_ring = gate_rows && q.gate >= 0;
   const int y_size = a.y_dt == WUSH_FP32 ? 4 : 2, r_size = a.r_dt == WUSH_FP32 ? 4 : 2,
             gate_size = a.gate_dt == WUSH_FP32 ? 4 : 2;
-  auto fill_y = [&](int i, int s) {                        // the CTA's row i into stage s
-    if (!a.y || i >= n_rows || tid >= (MODE == kAligned ? 1 : 32)) return;
-    const int64_t at = address(a.y, a.y_dt, a.y_stride, i);
-    char* to = smem + q.y + s * q.y_step;
-    const Units u = units(at, y_size, in_y);
-    if (tid == 0) {
-      sm100::mbar_arrive_expect_tx(&full[0][s], u.bytes);
-      bulk(at, u, to, &full[0][s]);
+  auto fill = [&](const void* p, int dt, int64_t stride, int size, const Bounds& in, int i, char* to, uint64_t* bar) {
+    const int64_t at = address(p, dt, stride, i);          // (by one warp, its first thread where no ends are left)
+    const Units u = units(at, size, in);
+    if (lane == 0) {
+      sm100::mbar_arrive_expect_tx(bar, u.bytes);
+      bulk(at, u, to, bar);
     }
-    if (MODE != kAligned) ends(at, y_size, u, to);
+    if (MODE != kAligned) ends(at, size, u, to);
+  };
+  const int role = MODE == kAligned && lane ? -1 : tid >> 5;
+  auto fill_y = [&](int i, int s) {                        // the CTA's row i into stage s
+    if (a.y && i < n_rows && role == 2) fill(a.y, a.y_dt, a.y_stride, y_size, in_y, i, smem + q.y + s * q.y_step, &full[0][s]);
   };
   auto fill_rest = [&](int i, int s) {
-    if (i >= n_rows || tid >= (MODE == kAligned ? 1 : 32)) return;
-    const int64_t at_r = r_ring ? address(a.r, a.r_dt, a.r_stride, i) : 0;
-    const int64_t at_g = gate_ring ? address(a.gate, a.gate_dt, a.gate_stride, i) : 0;
-    char* to_r = smem + q.r + s * q.r_step;
-    char* to_g = smem + q.gate + s * q.gate_step;
-    const Units u_r = r_ring ? units(at_r, r_size, in_r) : Units{0, 0}, u_g = gate_ring ? units(at_g, gate_size, in_g) : Units{0, 0};
-    if (tid == 0) {
-      sm100::mbar_arrive_expect_tx(&full[1][s], u_r.bytes + u_g.bytes);
-      if (r_ring) bulk(at_r, u_r, to_r, &full[1][s]);
-      if (gate_ring) bulk(at_g, u_g, to_g, &full[1][s]);
+    if (i >= n_rows) return;
+    if (role == 0) {
+      if (r_ring) fill(a.r, a.r_dt, a.r_stride, r_size, in_r, i, smem + q.r + s * q.r_step, &full[1][s]);
+      else if (lane == 0) sm100::mbar_arrive_expect_tx(&full[1][s], 0);
+    } else if (role == 1 && gate_ring) {
+      fill(a.gate, a.gate_dt, a.gate_stride, gate_size, in_g, i, smem + q.gate + s * q.gate_step, &full[1][s]);
     }
-    if (MODE != kAligned && r_ring) ends(at_r, r_size, u_r, to_r);
-    if (MODE != kAligned && gate_ring) ends(at_g, gate_size, u_g, to_g);
   };
   // (a wait that gives up marks the error and lets the CTA run on, so that its barriers
   // stay uniform; every later wait then gives up at once)
@@ -385,10 +383,8 @@ __global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __
     fill_rest(i, i);
   }
   // Meanwhile the vectors that every row uses, as fp32 and shifted like the rows; eight elements of
-  // each are asked for before any is stored.  (Where rows are shifted a vector is not, and its
-  // elements go to the threads one by one, so that a warp's lie side by side on both sides.)
-  constexpr int kVecMode = MODE == kAligned ? kAligned : kScalar;
-  const Columns<kVecMode> flat = {g, tid, d, 0, false};
+  // each are asked for before any is stored; shifted ones go to the threads one by one, so that a
+  // warp's lie side by side on both sides.
   Vectors post = {q.kept, nullptr, nullptr}, pre = post;
   const float* gate_vec = nullptr;
   if (q.kept) {
@@ -398,32 +394,71 @@ __global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __
     float* dst[5];
 #pragma unroll
     for (int n = 0; n < 5; ++n) dst[n] = src[n] ? reinterpret_cast<float*>(smem + q.vec[n]) + cols.shift : nullptr;
-    const bool alike = (!src[2] && !src[3] || !src[0] && !src[1] || dts[0] == dts[2]) && (!src[4] || dts[4] == dts[2]);
+    if constexpr (MODE == kAligned) {
+      const bool alike = (!src[2] && !src[3] || !src[0] && !src[1] || dts[0] == dts[2]) && (!src[4] || dts[4] == dts[2]);
 #pragma unroll 1
-    for (int j = 0; j < NV; ++j) {
-      float x[5][8];
-      if (alike) {
-        with_dtype(src[2] || src[3] || src[4] ? src[4] ? dts[4] : dts[2] : dts[0], [&](auto t) __attribute__((always_inline)) {
+      for (int j = 0; j < NV; ++j) {
+        float x[5][8];
+        if (alike) {
+          with_dtype(src[2] || src[3] || src[4] ? src[4] ? dts[4] : dts[2] : dts[0], [&](auto t) __attribute__((always_inline)) {
+#pragma unroll
+            for (int n = 0; n < 5; ++n)
+              if (src[n]) load_group<t.value, kAligned>(src[n], j, cols, x[n]);
+          });
+        } else {
 #pragma unroll
           for (int n = 0; n < 5; ++n)
-            if (src[n]) load_group<t.value, kVecMode, true>(src[n], j, flat, x[n]);
-        });
-      } else {
+            if (src[n])
+              with_dtype(dts[n], [&](auto t) __attribute__((always_inline)) {
+                load_group<t.value, kAligned>(src[n], j, cols, x[n]);
+              });
+        }
+#pragma unroll
+        for (int n = 0; n < 5; ++n)
+          if (src[n])
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int c = cols.at(j, e);
+              if (cols.has(c)) dst[n][c] = x[n][e] + offset[n];
+            }
+      }
+    } else {
+#pragma unroll 1
+      for (int j = 0; j < NV; ++j) {
+        uint32_t w[5][8];                                    // the vectors' bytes; converted once all are asked for
+#pragma unroll
+        for (int n = 0; n < 5; ++n) {
+          if (!src[n]) continue;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[n][e] = 0u;
+          if (dts[n] == WUSH_FP32) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int c = (j * 8 + e) * g + tid;
+              if (c < d) w[n][e] = static_cast<const uint32_t*>(src[n])[c];
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int c = (j * 8 + e) * g + tid;
+              if (c < d) w[n][e] = static_cast<const uint16_t*>(src[n])[c];
+            }
+          }
+        }
 #pragma unroll
         for (int n = 0; n < 5; ++n)
           if (src[n])
             with_dtype(dts[n], [&](auto t) __attribute__((always_inline)) {
-              load_group<t.value, kVecMode, true>(src[n], j, flat, x[n]);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int c = (j * 8 + e) * g + tid;
+                const float x = t.value == WUSH_FP32   ? __uint_as_float(w[n][e])
+                                : t.value == WUSH_BF16 ? bf16_lo(w[n][e])
+                                                       : __half2float(__ushort_as_half(static_cast<unsigned short>(w[n][e])));
+                if (c < d) dst[n][c] = x + offset[n];
+              }
             });
       }
-#pragma unroll
-      for (int n = 0; n < 5; ++n)
-        if (src[n])
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int c = flat.at(j, e);
-            if (flat.has(c)) dst[n][c] = x[n][e] + offset[n];
-          }
     }
     post.w = dst[0]; post.b = dst[1];
     pre.w = dst[2]; pre.b = dst[3];
@@ -565,7 +600,8 @@ int launch_ring(const Args& a, int sms, cudaStream_t st) {
   return launch_pdl(kern, static_cast<unsigned>(grid), G, smem, st, a, q);
 }
 
-// Threads of a row: 256 with up to 32 elements each, more for wide rows.
+// Threads of a row: 256 with up to 32 elements each (320 with 16 where those hold the row: a
+// third group for the last few columns would cost every thread), more for wide rows.
 template <int MODE>
 int launch_width(const Args& a, int sms, cudaStream_t st) {
   const int d = a.d + (MODE == kShifted ? 3 : 0);

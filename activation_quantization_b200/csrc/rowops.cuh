@@ -153,16 +153,15 @@ __device__ __forceinline__ void mask_edges(const Columns<MODE>& q, float (&v)[NV
 
 // A group of a row; columns that the row does not have read as zero.  In kShifted the row
 // lies in shared memory, where whole quads can be read at its ends, and their elements
-// outside the row are whatever lies there (mask_edges).  LOOSE: the row is a
-// vector in global memory whose quads need not be aligned with the matrices'.
-template <int DT, int MODE, bool LOOSE = false>
+// outside the row are whatever lies there (mask_edges).
+template <int DT, int MODE>
 __device__ __forceinline__ void load_group(const void* row, int j, const Columns<MODE>& q, float (&v)[8]) {
   using T = typename std::conditional<DT == WUSH_FP32, float, uint16_t>::type;
   const T* p = static_cast<const T*>(row);
   auto convert = [](uint32_t u) {
     return DT == WUSH_BF16 ? bf16_lo(u) : __half2float(__ushort_as_half(static_cast<unsigned short>(u)));
   };
-  if constexpr (MODE == kScalar || (MODE == kShifted && LOOSE)) {
+  if constexpr (MODE == kScalar) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int c = q.at(j, e);
