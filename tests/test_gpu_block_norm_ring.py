@@ -1,0 +1,110 @@
+"""The ring kernel of wush_norm and wush_residual_norm (more than 296 rows wider than 2048) against the
+formulas in fp64, over the types, forms and layouts that it tells apart.
+
+Tolerances, derived from the arithmetic, with u = 2^-24 (fp32's half step):
+  * a row's statistic sums at most 32 values in a thread, 5 shuffle steps and 32 warps, each rounded once,
+    on squares (2 more): 71 u relative, doubled for the rounded mean; F = 160 u covers it with the division
+    and the root;
+  * centring loses u-sized parts of the row's largest value, which the division by the row's deviation
+    magnifies: F max|v| / sigma absolute;
+  * exp(-g) is off by u |g| and two ulp (4 u), the quotient by two ulp (4 u), three roundings more: (11 + |g|) u;
+  * each further product or sum rounds once, and the output to its type: half its step.
+"""
+import itertools
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+U = 2.0 ** -24
+F = 160 * U
+TINY = {"bf16": 1e-38, "fp16": 2.0 ** -25, "fp32": 1e-38}       # half the subnormal step
+
+
+def norm64(v, e, kind, weight, bias, eps, offset):
+    """N(v) in fp64 and a bound on the error of its fp32 form, given the bound ``e`` on its input's."""
+    if kind == "none":
+        return v, e
+    c = v - v.mean(1, keepdim=True) if kind == "layer" else v
+    sigma = (c.square().mean(1, keepdim=True) + eps).sqrt()
+    top = (v.abs().amax(1, keepdim=True) * (F if kind == "layer" else 0) + e.amax(1, keepdim=True) * 2) / sigma
+    n = c / sigma
+    w = torch.ones_like(v[0]) if weight is None else weight.double() + offset
+    b = torch.zeros_like(v[0]) if bias is None else bias.double()
+    size = w.abs() + (0 if weight is None else 2 * abs(offset))
+    bound = (top * (1 + n.abs()) + F * n.abs()) * size + 4 * U * (n.abs() * size + b.abs())
+    return n * w + b, bound
+
+
+def close(got, want, dt, e):
+    step = float(torch.finfo(DT[dt]).eps) / 2
+    err = (got.double() - want).abs()
+    bad = ~(err <= step * (want.abs() + e) + e + TINY[dt])       # (a NaN is bad)
+    assert not bool(bad.any()), (int(bad.sum()), torch.nonzero(bad)[:4].tolist(), float(err.max()))
+
+
+def check(lib, rows, d, y="fp32", r="bf16", h="bf16", post="rms", pre="rms", gate=None, act="linear", a=1.0, b=1.0,
+          offset=0.0, eps=1e-6, post_w="bf16", post_b=None, pre_w="bf16", pre_b=None, gate_t=None, r_out="own",
+          want_h=True, view=lambda t, name: t):
+    """post_w, post_b, pre_w, pre_b: a type, or None for an absent vector; r_out: own, in place or None."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1000 * rows + d)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    vec = lambda t, one: None if t is None else (rand(d) * 0.5 + one).to(DT[t])  # noqa: E731
+    ty = view((rand(rows, d) + 0.25).to(DT[y]), "y")
+    tr = None if r is None else view((rand(rows, d) * 2).to(DT[r]), "r")
+    gt = gate_t or y
+    tg = None if gate is None else view((rand(rows, d) * 2).to(DT[gt]), "gate") if gate == "element" else \
+        (rand(d) * 2).to(DT[gt])
+    pw, pb, qw, qb = vec(post_w, 1), vec(post_b, 0), vec(pre_w, 1), vec(pre_b, 0)
+    y64, r64 = ty.double(), None if tr is None else tr.double()
+    out_t = r or "bf16"
+    nan = lambda dt, name: view(torch.full((rows, d), float("nan"), dtype=DT[dt], device="cuda"), name)  # noqa: E731
+    to = tr if r_out == "in place" else nan(out_t, "r_out") if r_out else None
+    th = nan(h, "h") if want_h else None
+    lib.wush_residual_norm(ty, tr, to, th, post=post, post_weight=pw, post_bias=pb, gate=tg, gate_act=act,
+                           residual_scale=a, branch_scale=b, pre=pre, pre_weight=qw, pre_bias=qb, eps=eps,
+                           weight_offset=offset)
+    assert lib.wush_check_device_status() == 0
+    u, e = norm64(y64, torch.zeros_like(y64), post, pw, pb, eps, offset)
+    if tg is not None:
+        g64 = tg.double()
+        f = g64 if act == "linear" else g64.sigmoid() if act == "sigmoid" else g64 * g64.sigmoid()
+        u, e = u * f, e * f.abs() + (11 + g64.abs()) * U * (u * f).abs()
+    o = b * u if r64 is None else a * r64 + b * u
+    e = abs(b) * e + 3 * U * ((b * u).abs() + (0 if r64 is None else (a * r64).abs()))
+    if r_out:
+        close(to, o, out_t, e)
+    if want_h:
+        want, e = norm64(o, e, pre, qw, qb, eps, offset)
+        close(th, want, h, e)
+
+
+TYPES = ("bf16", "fp16", "fp32")
+
+
+@pytest.mark.parametrize("gate_t", TYPES)
+@pytest.mark.parametrize("post_t", TYPES)
+@pytest.mark.parametrize("pre_t", TYPES)
+@pytest.mark.parametrize("d", [2560, 2561])
+def test_types_of_the_vectors(lib, d, post_t, pre_t, gate_t):
+    # every pairing of the types of a gate per channel and of both norms' vectors, each there or not
+    for pw, pb, qw, qb in itertools.product((0, 1), repeat=4):
+        check(lib, 298, d, gate="channel", gate_t=gate_t, post_w=post_t if pw else None, post_b=post_t if pb else None,
+              pre_w=pre_t if qw else None, pre_b=pre_t if qb else None)
+    for pw, pb in ((1, 0), (0, 1), (1, 1)):
+        check(lib, 298, d, gate="channel", gate_t=gate_t, post_w=post_t if pw else None, post_b=post_t if pb else None,
+              pre="none", pre_w=None)
+        check(lib, 298, d, gate="channel", gate_t=gate_t, post="none", post_w=None, pre_w=pre_t if pw else None,
+              pre_b=pre_t if pb else None)
+        check(lib, 298, d, gate="channel", gate_t=gate_t, post_w=post_t if pw else None,
+              post_b=post_t if pb else None, pre="none", pre_w=None, want_h=False)
+
+
+@pytest.mark.parametrize("d", [2304, 3584, 5120])
+def test_a_block_that_closes_with_a_scaled_norm_and_leaves_the_next_out(lib, d):
+    for post_t, gate_t in itertools.product(TYPES, TYPES):
+        check(lib, 400, d, gate="channel", gate_t=gate_t, post_w=post_t, pre="none", pre_w=None, want_h=False)
+        check(lib, 400, d, gate="channel", gate_t=gate_t, post_w=post_t, pre="rms", pre_w=None, r="fp32", h="fp16")
