@@ -108,3 +108,123 @@ def test_a_block_that_closes_with_a_scaled_norm_and_leaves_the_next_out(lib, d):
     for post_t, gate_t in itertools.product(TYPES, TYPES):
         check(lib, 400, d, gate="channel", gate_t=gate_t, post_w=post_t, pre="none", pre_w=None, want_h=False)
         check(lib, 400, d, gate="channel", gate_t=gate_t, post_w=post_t, pre="rms", pre_w=None, r="fp32", h="fp16")
+
+
+@pytest.mark.parametrize("y", TYPES)
+@pytest.mark.parametrize("r", TYPES + (None,))
+@pytest.mark.parametrize("d", [2560, 2051])
+def test_types_of_the_rows(lib, y, r, d):
+    for h in TYPES:
+        check(lib, 310, d, y, r, h, gate="element", gate_t="fp32" if h == "fp16" else "fp16", act="silu")
+        check(lib, 310, d, y, r, h, post="layer", pre="layer", post_b="bf16", pre_b="bf16")
+
+
+@pytest.mark.parametrize("post", ["none", "rms", "layer"])
+@pytest.mark.parametrize("pre", ["none", "rms", "layer"])
+@pytest.mark.parametrize("d", [2304, 2307])
+def test_forms(lib, post, pre, d):
+    # (1300 rows: every CTA's stages are refilled)
+    for gate, act in ((None, "linear"), ("channel", "silu"), ("element", "sigmoid"), ("element", "linear")):
+        for r_out, want_h in (("own", True), ("in place", True), (None, True), ("own", False), ("in place", False)):
+            check(lib, 1300, d, post=post, pre=pre, gate=gate, act=act, r_out=r_out, want_h=want_h, a=0.5, b=-1.75,
+                  offset=1.0)
+        check(lib, 1300, d, post=post, pre=pre, gate=gate, act=act, r=None)
+
+
+@pytest.mark.parametrize("d", [2560, 4097, 5124, 8200, 12288, 16390, 32765])
+def test_wide_rows_in_place(lib, d):
+    # (4 CTAs an SM at most: 1500 narrow rows and 700 wide ones come to each CTA's stages again)
+    rows = 1500 if d < 6000 else 700
+    check(lib, rows, d, gate="element", act="silu", r_out="in place")
+    check(lib, rows, d, "bf16", "fp16", "fp32", r_out="in place", post="none", post_w=None)
+    check(lib, rows, d, "fp32", "fp32", "bf16", post="layer", pre="layer", post_b="bf16", pre_b="bf16", gate="channel")
+
+
+def columns(rows_more, wide, at, kept):
+    """Tensors as columns of wider ones full of sevens (first column ``at[name]``), kept to be looked at."""
+    def view(t, name):
+        big = torch.full((t.shape[0] + rows_more, wide[name]), 7.0, dtype=t.dtype, device="cuda")
+        out = big[1:1 + t.shape[0], at[name]:at[name] + t.shape[1]]
+        out.copy_(t)
+        kept.append((big, at[name], t.shape))
+        return out
+    return view
+
+
+NAMES = ("y", "r", "r_out", "h", "gate")
+
+
+@pytest.mark.parametrize("rows", [300, 1300])
+@pytest.mark.parametrize("d, more, at", [(2304, 256, 128), (2304, 8, 8), (2304, 7, 3), (2305, 3, 2), (2307, 1, 0), (4101, 11, 5),
+                                         (2304, 4, 4), (8193, 2, 1)])
+def test_strided_rows_and_their_surroundings(lib, rows, d, more, at):
+    # every tensor is a block of columns of a wider one; nothing outside it is written
+    for kw in (dict(gate="element", act="sigmoid"), dict(r_out="in place", gate="channel"),
+               dict(y="bf16", r="fp32", h="fp16", post="layer", pre="layer"), dict(post="none", post_w=None, want_h=False)):
+        kept = []
+        check(lib, rows, d, view=columns(2, dict.fromkeys(NAMES, d + more), dict.fromkeys(NAMES, at), kept), **kw)
+        for big, first, (n, m) in kept:
+            big[1:1 + n, first:first + m] = 7.0
+            assert bool((big == 7.0).all())
+
+
+@pytest.mark.parametrize("rows", [300, 1300])
+@pytest.mark.parametrize("d", [2304, 2305, 4098, 6150])
+def test_tensors_whose_rows_begin_apart(lib, rows, d):
+    # row strides and first columns that agree in nothing: single elements
+    at = {"y": 1, "r": 2, "r_out": 3, "h": 5, "gate": 0}
+    wide = {k: d + 8 + v for k, v in at.items()}
+    for kw in (dict(), dict(post="layer", pre="layer", post_b="bf16", pre_b="bf16", gate="element", act="silu"),
+               dict(gate="channel", gate_t="fp32", r_out="in place"), dict(pre="none", pre_w=None, post_w="fp32", gate="channel")):
+        kept = []
+        check(lib, rows, d, view=columns(2, wide, at, kept), **kw)
+        for big, first, (n, m) in kept:
+            big[1:1 + n, first:first + m] = 7.0
+            assert bool((big == 7.0).all())
+
+
+@pytest.mark.parametrize("d", [2304, 2305])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_row_stays_its_own(lib, d, bad):
+    rows = 1300
+    y, r, gate = (torch.randn(rows, d, device="cuda") for _ in range(3))
+
+    def run(y, r, gate):
+        o, h = torch.empty_like(r), torch.empty_like(r)
+        lib.wush_residual_norm(y, r, o, h, post="rms", pre="layer", gate=gate, gate_act="silu")
+        return o, h
+
+    o, h = run(y, r, gate)
+    for which in range(3):
+        ins = [y.clone(), r.clone(), gate.clone()]
+        for row, col in ((0, 0), (7, d - 1), (650, d // 2), (rows - 1, d - 1)):
+            ins[which][row, col] = bad
+        o2, h2 = run(*ins)
+        keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+        keep[[0, 7, 650, rows - 1]] = False
+        assert torch.equal(o[keep], o2[keep]) and torch.equal(h[keep], h2[keep])
+        assert not bool(torch.isfinite(h2[~keep]).any())
+
+
+@pytest.mark.parametrize("d", [2304, 2305])
+def test_two_streams_and_a_graph(lib, d):
+    rows = 1300
+    side = torch.cuda.Stream()
+    y, r = torch.randn(rows, d, device="cuda"), torch.randn(rows, d, device="cuda").bfloat16()
+    outs = [[torch.empty_like(r) for _ in range(2)] for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        lib.wush_residual_norm(y, r, *outs[0], post="rms", pre="rms")
+        lib.wush_residual_norm(y, r, *outs[1], post="rms", pre="rms", stream=side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lib.wush_residual_norm(y, r, *outs[2], post="rms", pre="rms")
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for o in outs[1:] for a, b in zip(outs[0], o))
+    y.normal_()
+    g.replay()
+    lib.wush_residual_norm(y, r, *outs[0], post="rms", pre="rms")
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs[0], outs[2]))
