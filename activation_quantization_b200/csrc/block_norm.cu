@@ -541,6 +541,20 @@ int check_rows(const void* p, int dt, int64_t stride, int64_t rows, int64_t d, b
   return WUSH_OK;
 }
 
+// Whether an output's rows share a byte with a vector of ``bytes`` (one that lies between two
+// rows does not).
+bool on_vector(const Span& out, int64_t rows, const void* vector, int64_t bytes) {
+  const char* v = static_cast<const char*>(vector);
+  if (!out.p || !v || v >= out.p + (rows - 1) * out.stride + out.width || out.p >= v + bytes) return false;
+  const int64_t behind = ((v - out.p) % out.stride + out.stride) % out.stride;     // of a row's first byte
+  return behind < out.width || behind + bytes > out.stride;
+}
+
+bool on_norm(const Span& out, int64_t rows, const NormArgs& n, int64_t d) {
+  const int64_t bytes = d * dtype_bytes(n.dt);
+  return on_vector(out, rows, n.w, bytes) || on_vector(out, rows, n.b, bytes);
+}
+
 constexpr int kSmemPerSm = 224 * 1024;                     // what the rings of an SM's CTAs share
 constexpr int kCtaOverhead = 3 * 1024;                     // static and reserved shared memory of a CTA
 constexpr int kInFlight = 96 * 1024;                       // bytes of rows that an SM asks for ahead
@@ -705,11 +719,10 @@ extern "C" int wush_residual_norm(const wush_residual_norm_args* args, void* str
       overlap(sh, sr, rows) || overlap(sh, so, rows))
     return WUSH_ERR_INVALID_ARG;
   for (const Span& out : {so, sh}) {
-    if (!q.gate || !out.p) continue;
-    const char* g = static_cast<const char*>(q.gate);
+    if (on_norm(out, rows, a.post, d) || on_norm(out, rows, a.pre, d)) return WUSH_ERR_INVALID_ARG;
     // (a gate per channel is one row, read by every row)
     if (q.gate_stride ? overlap(out, span(q.gate, q.gate_dtype, q.gate_stride, d), rows)
-                      : out.p < g + d * dtype_bytes(q.gate_dtype) && g < out.p + (rows - 1) * out.stride + out.width)
+                      : on_vector(out, rows, q.gate, d * dtype_bytes(q.gate_dtype)))
       return WUSH_ERR_INVALID_ARG;
   }
   a.y = q.y; a.y_dt = q.y_dtype; a.y_stride = q.y_stride;
@@ -734,7 +747,8 @@ extern "C" int wush_norm(const void* x, int x_dtype, int64_t x_stride, int64_t r
   if ((st = check_norm(norm, &a.pre, &vec)) != WUSH_OK) return st;
   if (rows == 0) return WUSH_OK;
   const bool in_place = x == h && x_dtype == h_dtype && x_stride == h_stride;
-  if (!in_place && overlap(span(h, h_dtype, h_stride, d), span(x, x_dtype, x_stride, d), rows))
+  const Span sh = span(h, h_dtype, h_stride, d);
+  if ((!in_place && overlap(sh, span(x, x_dtype, x_stride, d), rows)) || on_norm(sh, rows, a.pre, d))
     return WUSH_ERR_INVALID_ARG;
   a.r = x; a.r_dt = x_dtype; a.r_stride = x_stride;
   a.h = h; a.h_dt = h_dtype; a.h_stride = h_stride;

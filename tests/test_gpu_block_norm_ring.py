@@ -228,3 +228,16 @@ def test_two_streams_and_a_graph(lib, d):
     lib.wush_residual_norm(y, r, *outs[0], post="rms", pre="rms")
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs[0], outs[2]))
+
+
+def test_a_weight_between_an_outputs_rows(lib):
+    # it shares no byte with them
+    rows, d = 300, 2304
+    x = torch.randn(rows, d, device="cuda").bfloat16()
+    big = torch.ones(rows, 2 * d, dtype=torch.bfloat16, device="cuda")
+    w = big[3, d:]
+    w.copy_(torch.rand(d, device="cuda"))
+    h = torch.empty_like(x)
+    lib.wush_norm(x, h, "rms", w)
+    lib.wush_norm(x, big[:, :d], "rms", w)
+    assert torch.equal(big[:, :d], h)
