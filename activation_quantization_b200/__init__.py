@@ -539,12 +539,14 @@ def wush_norm(x, h, kind, weight=None, bias=None, eps: float = 1e-6, weight_offs
 
 def wush_residual_norm(y, r=None, r_out=None, h=None, *, post="none", post_weight=None, post_bias=None, gate=None,
                        gate_act="linear", residual_scale: float = 1.0, branch_scale: float = 1.0, pre="none",
-                       pre_weight=None, pre_bias=None, eps: float = 1e-6, weight_offset: float = 0.0, stream=None):
+                       pre_weight=None, pre_bias=None, eps: float = 1e-6, weight_offset: float = 0.0, stream=None,
+                       pre_eps: float | None = None, pre_weight_offset: float | None = None):
     """r_out = residual_scale * r + branch_scale * N_post(y) * act(gate); h = N_pre(r_out).
 
     y, r, r_out, h: CUDA [rows, d] (bf16, fp32 or fp16 each, r_out of r's type; rows contiguous,
     any row stride); r_out may be r; r, r_out or h may be None.  gate: CUDA [d] (one for all
-    rows), [rows, d] or None.  eps and weight_offset hold for both norms."""
+    rows), [rows, d] or None.  eps and weight_offset hold for both norms, unless pre_eps or
+    pre_weight_offset gives the pre-norm its own."""
     fn = "wush_residual_norm"
     dev, shape = _device_call(y), y.shape
     yp, yd, ys = _rows(fn, "y", y, shape, dev)
@@ -566,7 +568,8 @@ def wush_residual_norm(y, r=None, r_out=None, h=None, *, post="none", post_weigh
     args = _RESIDUAL_NORM_ARGS.pack(
         yp, gp, rp, op, hp, ys, gs, rs, os_, hs, rows, d,
         *_norm_spec(fn, "the post", post, post_weight, post_bias, d, dev, eps, weight_offset),
-        *_norm_spec(fn, "the pre", pre, pre_weight, pre_bias, d, dev, eps, weight_offset),
+        *_norm_spec(fn, "the pre", pre, pre_weight, pre_bias, d, dev, eps if pre_eps is None else pre_eps,
+                    weight_offset if pre_weight_offset is None else pre_weight_offset),
         yd, gd, rd, hd, GATES[gate_act], residual_scale, branch_scale)
     if rows:                                        # (an empty tensor has no pointer)
         _launch(_lib.wush_residual_norm, fn, (args,), dev, stream)
