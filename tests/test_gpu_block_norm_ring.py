@@ -241,3 +241,18 @@ def test_a_weight_between_an_outputs_rows(lib):
     lib.wush_norm(x, h, "rms", w)
     lib.wush_norm(x, big[:, :d], "rms", w)
     assert torch.equal(big[:, :d], h)
+
+
+@pytest.mark.parametrize("rows, d", [(3, 8), (3, 4096), (300, 2304), (300, 2305), (300, 32768)])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_the_ends_of_the_range_of_squares(lib, rows, d, kind):
+    # the root of the sum of squares just below 1.8e19; eps = 0 and the root of their mean just above 1.1e-19
+    x = torch.randn(rows, d, device="cuda", dtype=torch.float64)
+    if kind == "layer":
+        x -= x.mean(1, keepdim=True)
+    for v in (x / x.square().sum(1, keepdim=True).sqrt() * 1.7e19, x / x.square().mean(1, keepdim=True).sqrt() * 2e-19):
+        v = v.float()
+        h = torch.empty_like(v)
+        lib.wush_norm(v, h, kind, eps=0.0)
+        want, e = norm64(v.double(), torch.zeros_like(x), kind, None, None, 0.0, 0.0)
+        close(h, want, "fp32", e)
