@@ -79,7 +79,6 @@ struct Ring {
   int y_step, r_step, gate_step;                           // from one stage to the next
   int vec[5];                                              // post w, post b, pre w, pre b, gate per channel
   bool kept;                                               // the vectors are in shared memory
-  int vec_dt;                                              // the type that all the vectors have, or -1
 };
 
 __device__ __forceinline__ float activate(float g, int act) {
@@ -396,11 +395,15 @@ __global__ void __launch_bounds__(G, ring_ctas(NV, G)) norm_ring_kernel(const __
 #pragma unroll
     for (int n = 0; n < 5; ++n) dst[n] = src[n] ? reinterpret_cast<float*>(smem + q.vec[n]) + cols.shift : nullptr;
     if constexpr (MODE == kAligned) {
+      // whether all vectors have one type (that of an absent one says nothing)
+      const bool has_post = src[0] || src[1], has_pre = src[2] || src[3];
+      const bool alike = (!has_post || !has_pre || dts[0] == dts[2]) &&
+                         (!src[4] || ((!has_pre || dts[4] == dts[2]) && (!has_post || dts[4] == dts[0])));
 #pragma unroll 1
       for (int j = 0; j < NV; ++j) {
         float x[5][8];
-        if (q.vec_dt >= 0) {
-          with_dtype(q.vec_dt, [&](auto t) __attribute__((always_inline)) {
+        if (alike) {
+          with_dtype(src[4] ? dts[4] : has_pre ? dts[2] : dts[0], [&](auto t) __attribute__((always_inline)) {
 #pragma unroll
             for (int n = 0; n < 5; ++n)
               if (src[n]) load_group<t.value, kAligned>(src[n], j, cols, x[n]);
@@ -583,17 +586,8 @@ int plan(const Args& a, bool aligned, int ctas, Ring* q) {
   if (q->stages < 1) q->stages = 1;
   if (q->stages > kMaxStages) q->stages = kMaxStages;
   const void* vecs[5] = {a.post.w, a.post.b, a.pre.w, a.pre.b, gate_rows ? nullptr : a.gate};
-  const int dts[5] = {a.post.dt, a.post.dt, a.pre.dt, a.pre.dt, a.gate_dt};
   int all = 0;
-  q->vec_dt = -1;
-  bool alike = true;                                       // (an absent vector's type says nothing)
-  for (int k = 0; k < 5; ++k) {
-    if (!vecs[k]) continue;
-    all += up(int64_t(a.d) * 4 + edge);
-    alike = alike && (q->vec_dt < 0 || q->vec_dt == dts[k]);
-    q->vec_dt = dts[k];
-  }
-  if (!alike) q->vec_dt = -1;
+  for (int k = 0; k < 5; ++k) all += vecs[k] ? up(int64_t(a.d) * 4 + edge) : 0;
   q->kept = all + q->stages * stage <= budget;             // otherwise they are read from L2, row by row
   int at = 0;
   q->y = at; q->y_step = y; at += y * q->stages;
