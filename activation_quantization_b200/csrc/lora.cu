@@ -61,6 +61,8 @@ struct LoraArgs {
   int64_t x_stride, y_in_stride, y_stride;
   int64_t tokens;
   int d_in, d_out, n_adapters, rank;
+  int64_t polls;                                           // see kDefaultPolls
+  bool mute;                                               // test hook: shrink and expand ask for no operands
 };
 
 template <typename E>
@@ -785,11 +787,14 @@ __device__ __forceinline__ void tma_tile_b(uint32_t dst, const CUtensorMap* map,
       : "memory");
 }
 
-// A wait that gives up sets the CTA's flag, and every later wait then gives up at once: the
-// roles run on to the CTA's common barriers, and the error is reported at the end.
-__device__ __forceinline__ void wait_or_flag(uint64_t* bar, uint32_t parity, int* abort_flag) {
-  if (!sm100::mbar_wait_bounded(bar, parity, kDefaultPolls, kDeadlineNs, abort_flag))
-    *static_cast<volatile int*>(abort_flag) = 1;
+// False for a wait that gives up: it sets the CTA's flag, by which the other roles' waits give up
+// too.  The thread then asks for nothing more (its roles' barriers are not through their turns), and
+// its warp runs on to the CTA's common barriers, where the error is reported and what is in
+// flight lands.
+__device__ __forceinline__ bool wait_or_flag(uint64_t* bar, uint32_t parity, const LoraArgs& p, int* abort_flag) {
+  if (sm100::mbar_wait_bounded(bar, parity, p.polls, kDeadlineNs, abort_flag)) return true;
+  *static_cast<volatile int*>(abort_flag) = 1;
+  return false;
 }
 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -915,20 +920,21 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __gri
       rows[j] = mine && row + j < count ? w.token[tile.y + row + j] : none;
       block = block && rows[j] == rows[0] + j;
     }
+    bool live = !p.mute;
     for (int i = 0; i < n; ++i) {
       const int s = i % L::kStages, col = (first + i) * kBk;
-      wait_or_flag(&empty[s], ((i / L::kStages) & 1) ^ 1, &abort_flag);
+      live = live && wait_or_flag(&empty[s], ((i / L::kStages) & 1) ^ 1, p, &abort_flag);
       const uint32_t to = base + s * L::kStage;
-      if (lane == 0) {
+      if (lane == 0 && live) {
         sm100::mbar_arrive_expect_tx(&full[s], 2 * (R + groups * 8) * 128);
         tma_tile(to + kTile * 128, &map_a, col, tile.x * p.rank, &full[s]);
         tma_tile(to + L::kHalf + kTile * 128, &map_a, col + 64, tile.x * p.rank, &full[s]);
       }
       __syncwarp();
       const uint32_t dst = to + half * L::kHalf + row * 128;
-      if (mine && block) {
+      if (mine && block && live) {
         tma_tile(dst, &map_x8, col + half * 64, rows[0], &full[s]);
-      } else if (mine) {
+      } else if (mine && live) {
         tma_gather4(dst, &map_x, col + half * 64, make_int4(rows[0], rows[1], rows[2], rows[3]), &full[s]);
         tma_gather4(dst + 512, &map_x, col + half * 64, make_int4(rows[4], rows[5], rows[6], rows[7]), &full[s]);
       }
@@ -938,8 +944,8 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __gri
       const uint32_t idesc = idesc_f16_m64<E>(ranks16);
       for (int i = 0; i < n; ++i) {
         const int s = i % L::kStages, chain = i / kChain, d = chain % L::kAcc;
-        if (i % kChain == 0) wait_or_flag(&d_empty[d], ((chain / L::kAcc) & 1) ^ 1, &abort_flag);
-        wait_or_flag(&full[s], (i / L::kStages) & 1, &abort_flag);
+        if (i % kChain == 0 && !wait_or_flag(&d_empty[d], ((chain / L::kAcc) & 1) ^ 1, p, &abort_flag)) break;
+        if (!wait_or_flag(&full[s], (i / L::kStages) & 1, p, &abort_flag)) break;
         sm100::tc_fence_after();
         const uint32_t at = base + s * L::kStage;
 #pragma unroll
@@ -953,9 +959,10 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __gri
     }
     __syncwarp();
   } else if (warp < 4) {
+    bool live = true;
     for (int chain = 0; chain * kChain < n; ++chain) {
       const int d = chain % L::kAcc;
-      wait_or_flag(&d_full[d], (chain / L::kAcc) & 1, &abort_flag);
+      live = live && wait_or_flag(&d_full[d], (chain / L::kAcc) & 1, p, &abort_flag);
       sm100::tc_fence_after();
 #pragma unroll
       for (int b = 0; b < R / 8; b += 4) {                 // (four loads in flight)
@@ -977,6 +984,7 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __gri
     }
   }
   __syncthreads();                                         // the stages have been read: s goes over them
+  if (tid == 0 && *static_cast<volatile int*>(&abort_flag)) report_timeout();
   if (warp < 4) {
 #pragma unroll
     for (int b = 0; b < R / 8; ++b) {                      // (columns from ranks16 on are never read)
@@ -1035,7 +1043,6 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __gri
     }
   }
   sm100::cluster_sync();                                   // no CTA leaves while another may read its sums
-  if (tid == 0 && *static_cast<volatile int*>(&abort_flag)) report_timeout();
 }
 
 // A CTA goes along a tile in blocks of 64 columns: D = B s is one 64 x 64 product in TMEM.
@@ -1144,14 +1151,15 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
       if (++i == slots) i = 0, turn ^= 1;
     }
   };
-  // Calls f for each stretch of a piece within one tile, piece after piece, until none is left.
+  // Calls f for each stretch of a piece within one tile, piece after piece, until none is left
+  // (or given out: a wait gave up).
   auto for_pieces = [&](auto f) __attribute__((always_inline)) {
     for (;; ++turn) {
-      wait_or_flag(&piece_full[turn & 1], (turn >> 1) & 1, &abort_flag);
+      if (!__all_sync(0xffffffffu, wait_or_flag(&piece_full[turn & 1], (turn >> 1) & 1, p, &abort_flag))) return;
       int64_t pos = piece[turn & 1] * size;
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(&piece_empty[turn & 1]);
-      if (pos >= all || *static_cast<volatile int*>(&abort_flag)) return;
+      if (pos >= all) return;
       const int64_t to = pos + size < all ? pos + size : all;
       while (pos < to) {
         Piece q;
@@ -1169,10 +1177,11 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
     if (lane == 0) {
       unsigned index = blockIdx.x;
       for (int i = 0;; ++i) {
-        wait_or_flag(&piece_empty[i & 1], ((i >> 1) & 1) ^ 1, &abort_flag);
+        if (!wait_or_flag(&piece_empty[i & 1], ((i >> 1) & 1) ^ 1, p, &abort_flag)) break;
+        if (*static_cast<volatile int*>(&abort_flag)) break;
         piece[i & 1] = index;
         sm100::mbar_arrive(&piece_full[i & 1]);
-        if (index * size >= all || *static_cast<volatile int*>(&abort_flag)) break;
+        if (index * size >= all) break;
         index = gridDim.x + atomicAdd(&w.counts->next, 1u);
       }
     }
@@ -1180,13 +1189,14 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
   } else
   if (warp == 8) {
     int ns = 0;                                            // tiles' terms asked for so far
+    bool live = !p.mute;
     Slot slot = {0, 1};                                    // of B
     for_pieces([&](const Piece& q) {
       const int k = q.tile.w, units = (k + 63) / 64;
       if (k == 0) return;
-      wait_or_flag(&s_empty, (ns & 1) ^ 1, &abort_flag);
+      live = live && wait_or_flag(&s_empty, (ns & 1) ^ 1, p, &abort_flag);
       ++ns;
-      if (lane == 0) {
+      if (lane == 0 && live) {
         sm100::mbar_arrive_expect_tx(&s_full, l.terms_bytes);
         for (int i = 0; i < l.terms_bytes / (kTile * 128); ++i)
           tma_tile(s_base + i * (kTile * 128), &map_s, i * 64, q.tile.y, &s_full);
@@ -1194,28 +1204,29 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
       const int row8 = static_cast<int>(static_cast<int64_t>(q.tile.x) * p.d_out / 8) + q.first * (kCols / 8);
       for (int b = 0; b < q.blocks; ++b, slot.next(l.b_slots)) {
         const int s = slot.i;
-        wait_or_flag(&b_empty[s], slot.turn, &abort_flag);
-        if (lane == 0) sm100::mbar_arrive_expect_tx(&b_full[s], units * kCols * 128);
+        live = live && wait_or_flag(&b_empty[s], slot.turn, p, &abort_flag);
+        if (lane == 0 && live) sm100::mbar_arrive_expect_tx(&b_full[s], units * kCols * 128);
         __syncwarp();
         // (columns beyond d_out read the next adapter's rows; their results are not stored)
-        for (int i = lane; i < units * 4; i += 32)
+        for (int i = live ? lane : units * 4; i < units * 4; i += 32)
           tma_tile_b(b_ring + s * l.b_bytes + (i >> 2) * (kCols * 128) + (i & 3) * 2048, &map_b, (i >> 2) * 64,
                      row8 + b * (kCols / 8) + (i & 3) * 2, &b_full[s]);
       }
     });
   } else if (warp == 9) {
     int nb = 0, ns = 0;
+    bool live = true;
     Slot slot = {0, 0};
     constexpr uint32_t idesc = idesc_f16_m64<E>(kCols);
     for_pieces([&](const Piece& q) {
       const int k = q.tile.w, kp = (k + 15) / 16 * 16;
       if (k == 0) return;
-      wait_or_flag(&s_full, ns & 1, &abort_flag);
+      live = live && wait_or_flag(&s_full, ns & 1, p, &abort_flag);
       ++ns;
       for (int b = 0; b < q.blocks; ++b, ++nb, slot.next(l.b_slots)) {
         const int s = slot.i, d = nb & 1;
         const uint32_t at = b_ring + s * l.b_bytes;
-        wait_or_flag(&b_full[s], slot.turn, &abort_flag);
+        live = live && wait_or_flag(&b_full[s], slot.turn, p, &abort_flag);
         if (k < kp) {
           // columns from k on are padding that may hold anything: the last step's become zero
           for (int r = lane; r < kCols; r += 32)
@@ -1225,9 +1236,9 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
           sm100::fence_proxy_async_smem();
           __syncwarp();
         }
-        wait_or_flag(&d_empty[d], ((nb >> 1) & 1) ^ 1, &abort_flag);
+        live = live && wait_or_flag(&d_empty[d], ((nb >> 1) & 1) ^ 1, p, &abort_flag);
         sm100::tc_fence_after();
-        if (lane == 0) {
+        if (lane == 0 && live) {
           for (int t = 0; t < kT; ++t)
             for (int ks = 0; ks < kp; ks += 16) {
               const int pos_k = t * w.row_elems + ks;
@@ -1245,6 +1256,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
   } else {
     const int wm = warp & 3, wn = warp >> 2, g = lane >> 2, c = lane & 3;
     const bool in_place = p.y == p.y_in;
+    bool live = true;
     int nb = 0;
     for_pieces([&](const Piece& q) {
       const int k = q.tile.w, count = q.tile.z;
@@ -1286,7 +1298,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
         float acc[4][4] = {};
         if (k) {
           const int d = nb & 1;
-          wait_or_flag(&d_full[d], (nb >> 1) & 1, &abort_flag);
+          live = live && wait_or_flag(&d_full[d], (nb >> 1) & 1, p, &abort_flag);
           ++nb;
           if (some) {
             sm100::tc_fence_after();
@@ -1337,11 +1349,14 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
   }
   sm100::tc_fence_before();
   __syncthreads();
+  if (*static_cast<volatile int*>(&abort_flag)) {          // (the same for all threads: no role waits any more)
+    if (tid == 0) report_timeout();
+    __syncthreads();
+  }
   if (warp == 8) {
     sm100::tc_fence_after();
     sm100::tmem_dealloc(tmem, 2 * kD);
   }
-  if (tid == 0 && *static_cast<volatile int*>(&abort_flag)) report_timeout();
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1542,7 +1557,8 @@ extern "C" int wush_lora_add(const wush_lora_args* args, void* stream) {
     return WUSH_ERR_INVALID_ARG;
   LoraArgs p = {q.x, q.adapter, q.a, q.b, q.ranks, q.scale, q.y_in, q.y, q.x_stride, q.y_in_stride, q.y_stride,
                 q.tokens, static_cast<int>(q.d_in), static_cast<int>(q.d_out), static_cast<int>(q.n_adapters),
-                static_cast<int>(q.rank)};
+                static_cast<int>(q.rank), g_wait_limit_override > 0 ? g_wait_limit_override : kDefaultPolls,
+                g_wait_limit_override > 0};
   const size_t need = wush_lora_workspace_bytes(q.tokens, q.d_in, q.d_out, q.n_adapters, q.rank);
   if (need) {
     if (!q.workspace || !aligned16(q.workspace)) return WUSH_ERR_INVALID_ARG;

@@ -569,9 +569,11 @@ size_t wush_lora_workspace_bytes(int64_t tokens, int64_t d_in, int64_t d_out, in
  * WUSH_ERR_CUDA if the stream itself reports an error. */
 int wush_check_device_status(void* stream);
 
-/* Test hook: makes the next wush_qgemm launches give up their first barrier wait
- * after ``max_polls`` polls (0 restores the default limit) so that the timeout
- * path can be exercised without hanging anything. */
+/* Test hook: makes the next wush_qgemm, wush_norm, wush_residual_norm and wush_lora_add
+ * launches give up their first barrier wait after ``max_polls`` polls, since nothing
+ * arrives there (the kernels for few rows of the norms and adapters have no such waits),
+ * and limits the other kernels' waits to as many polls (0 restores the default
+ * limit), so that the timeout path can be exercised without hanging anything. */
 int wush_debug_set_wait_limit(int64_t max_polls);
 
 /* Test hook: 0 (default) lets wush_qgemm use CTA-pair (cta_group::2) 256 x 256
