@@ -82,9 +82,13 @@ struct Ring {
   bool kept;                                               // the vectors are in shared memory
 };
 
+// The exponential is 2^t with t = -g log2 e rounded to fp32, the quotient within 2 ulp: some
+// (10 + |g|) 2^-24 of the result, which outputs of 16 bits do not see.  With expf and a rounded reciprocal
+// instead, 4096 rows x 5120 with a gate per channel take 54.0 us (44.6 so), 1531 x 4097 with a gate per
+// element 28.9 (23.6), 8192 x 1024 31.4 (24.7); with expf alone 48.2, 24.4 and 29.4.
 __device__ __forceinline__ float activate(float g, int act) {
   if (act == WUSH_GATE_LINEAR) return g;
-  const float s = __fdividef(1.0f, 1.0f + __expf(-g));     // (0 where the exponential overflows)
+  const float s = __fdividef(1.0f, 1.0f + __expf(-g));     // (0 where the sum is above 2^126)
   return act == WUSH_GATE_SIGMOID ? s : g * s;
 }
 

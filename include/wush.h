@@ -437,13 +437,14 @@ int itq3_dequant_gemv_noalloc(const uint8_t* codes, const void* scales_fp16, con
  *   NONE:  v
  * (no weight: a factor of 1, weight_offset unused; no bias: 0).  Everything is fp32
  * inside: h is taken from the fp32 sum, not from the rounded r_out, and each output
- * is rounded once.  Sums are fp32 too.  So the root of a row's sum of squares (LAYER:
+ * is rounded once.  sigmoid(g) is within (10 + |g|) 2^-24 of its value, and 0 where that
+ * is below 1.2e-38.  Sums are fp32 too.  So the root of a row's sum of squares (LAYER:
  * of deviations from the mean) has to stay below 1.8e19, which values up to 9e16
  * do at any width: beyond it N gives 0, or b, for finite values.  With eps = 0 the root of
  * the mean of squares has to be 1.1e-19 at least.  LAYER's mean is off by at most
  * 2^-17 of the row's largest magnitude (some 2^-23 as a rule), which shows where the
- * row's deviation is small beside that.  A NaN or an infinity reaches its own row only.  A row of zeros with
- * eps = 0 gives NaN, as the formula does.
+ * row's deviation is small beside that.  A NaN or an infinity reaches its own row
+ * only.  A row of zeros with eps = 0 gives NaN, as the formula does.
  * ------------------------------------------------------------------------- */
 
 /* Element types of the calls from here on (the first two are WUSH_IN_BF16 and

@@ -256,3 +256,18 @@ def test_the_ends_of_the_range_of_squares(lib, rows, d, kind):
         lib.wush_norm(v, h, kind, eps=0.0)
         want, e = norm64(v.double(), torch.zeros_like(x), kind, None, None, 0.0, 0.0)
         close(h, want, "fp32", e)
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+@pytest.mark.parametrize("d", [4, 2304])
+def test_gates_over_their_whole_range(lib, act, d):
+    rows = 400
+    g = torch.linspace(-110, 110, rows * d, device="cuda").view(rows, d)
+    g[0, :3] = torch.tensor([0.0, float("inf"), -3e38], device="cuda")
+    one, u = torch.ones(rows, d, device="cuda"), torch.empty(rows, d, device="cuda")
+    lib.wush_residual_norm(one, None, u, gate=g, gate_act=act)
+    want = 1 / (1 + (-g.double()).exp()) * (g.double() if act == "silu" else 1)
+    # the bound on the sigmoid, silu's product, and what is below 1.2e-38 as 0
+    bound = (11 + g.double().abs()) * U * want.abs() + 1.2e-38 * (g.double().abs() if act == "silu" else 1)
+    ok = ((u.double() - want).abs() <= bound) | (u.double() == want)
+    assert bool(ok.all()), torch.nonzero(~ok)[:4].tolist()
