@@ -82,6 +82,9 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 
 template <typename E>
 struct Split;
+// The tensor core's additions cut off low bits of the larger operand's, so where terms share a sum the low
+// ones go first: of the 48 steps that 256 ranks take, the 32 of bf16's second and third term then work on
+// sums of 2^-7 of the result's size, and 16 on the whole.
 template <>
 struct Split<__nv_bfloat16> {
   static constexpr int kTerms = 3, kSums = 1;              // kSums: sums that the terms' products go to
@@ -494,11 +497,12 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(MB))
     for (int u = 0; u < kUnroll; ++u) {
       const int n0 = (nb + u) * 16 + row, n1 = n0 + 8;
       float o[Split<E>::kSums][4] = {};
+      // (the low terms first: see Split)
 #pragma unroll
-      for (int m = 0; m < kM; ++m) {
-        if (m * kPair * 16 >= k) break;
+      for (int q = kT - 1; q >= 0; --q) {
 #pragma unroll
-        for (int q = 0; q < kT; ++q) {
+        for (int m = 0; m < kM; ++m) {
+          if (m * kPair * 16 >= k) break;
           const Piece s = kHeld ? held[kHeld ? m : 0][q] : term(m, q);
 #pragma unroll
           for (int e = 0; e < kPair; ++e) {
@@ -832,8 +836,8 @@ constexpr int kBk = 128;                                  // columns of d_in a s
 // take D out of TMEM.  A stage holds 128 columns as two halves of 64, rows of 128 bytes with
 // the 128-byte swizzle.  D is added to fp32 registers and begun anew every kChain stages: the
 // tensor core's own additions cut off low bits, and 32 of them in a row stay near fp32's
-// rounding of the sums (4096 tokens x 12288, rank 128: a chain over a CTA's whole d_in gave
-// 2.8e-6 relative to the result, chains of 32 give 1.0e-6).
+// rounding of the sums (4096 tokens x 12288, rank 128: 5.7e-7 relative to the result; with
+// the second product's low terms last, when both were measured, 1.0e-6, and 2.8e-6 with a chain over a CTA's whole d_in).
 //
 // What bounds it: 4096 tokens x 12288, rank 64, read 113 MB from DRAM and 282 MB from L2 (A
 // once a tile) in some 31 us, the tensor pipe active for a quarter of it.
@@ -1239,12 +1243,12 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
         live = live && wait_or_flag(&d_empty[d], ((nb >> 1) & 1) ^ 1, p, &abort_flag);
         sm100::tc_fence_after();
         if (lane == 0 && live) {
-          for (int t = 0; t < kT; ++t)
+          for (int t = kT - 1; t >= 0; --t)                // (the low terms first: see Split)
             for (int ks = 0; ks < kp; ks += 16) {
               const int pos_k = t * w.row_elems + ks;
               tc_mma(tmem + d * kD + t % kSums * kCols, s_base + (pos_k >> 6) * (kTile * 128) + (pos_k & 63) * 2,
                      at + (ks >> 6) * (kCols * 128) + (ks & 63) * 2, idesc,
-                     t >= kSums || ks > 0);
+                     t < kT - kSums || ks > 0);
             }
           sm100::tc_commit(&b_empty[s]);
           sm100::tc_commit(&d_full[d]);
