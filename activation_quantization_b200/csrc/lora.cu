@@ -1198,7 +1198,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
     for_pieces([&](const Piece& q) {
       const int k = q.tile.w, units = (k + 63) / 64;
       if (k == 0) return;
-      live = live && wait_or_flag(&s_empty, (ns & 1) ^ 1, p, &abort_flag);
+      if (!wait_or_flag(&s_empty, (ns & 1) ^ 1, p, &abort_flag)) live = false;
       ++ns;
       if (lane == 0 && live) {
         sm100::mbar_arrive_expect_tx(&s_full, l.terms_bytes);
@@ -1208,7 +1208,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
       const int row8 = static_cast<int>(static_cast<int64_t>(q.tile.x) * p.d_out / 8) + q.first * (kCols / 8);
       for (int b = 0; b < q.blocks; ++b, slot.next(l.b_slots)) {
         const int s = slot.i;
-        live = live && wait_or_flag(&b_empty[s], slot.turn, p, &abort_flag);
+        if (!wait_or_flag(&b_empty[s], slot.turn, p, &abort_flag)) live = false;
         if (lane == 0 && live) sm100::mbar_arrive_expect_tx(&b_full[s], units * kCols * 128);
         __syncwarp();
         // (columns beyond d_out read the next adapter's rows; their results are not stored)
@@ -1225,12 +1225,12 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
     for_pieces([&](const Piece& q) {
       const int k = q.tile.w, kp = (k + 15) / 16 * 16;
       if (k == 0) return;
-      live = live && wait_or_flag(&s_full, ns & 1, p, &abort_flag);
+      if (!wait_or_flag(&s_full, ns & 1, p, &abort_flag)) live = false;
       ++ns;
       for (int b = 0; b < q.blocks; ++b, ++nb, slot.next(l.b_slots)) {
         const int s = slot.i, d = nb & 1;
         const uint32_t at = b_ring + s * l.b_bytes;
-        live = live && wait_or_flag(&b_full[s], slot.turn, p, &abort_flag);
+        if (!wait_or_flag(&b_full[s], slot.turn, p, &abort_flag)) live = false;
         if (k < kp) {
           // columns from k on are padding that may hold anything: the last step's become zero
           for (int r = lane; r < kCols; r += 32)
@@ -1240,15 +1240,16 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
           sm100::fence_proxy_async_smem();
           __syncwarp();
         }
-        live = live && wait_or_flag(&d_empty[d], ((nb >> 1) & 1) ^ 1, p, &abort_flag);
+        if (!wait_or_flag(&d_empty[d], ((nb >> 1) & 1) ^ 1, p, &abort_flag)) live = false;
         sm100::tc_fence_after();
         if (lane == 0 && live) {
-          for (int t = kT - 1; t >= 0; --t)                // (the low terms first: see Split)
+          for (int i = 0; i < kT; ++i)
             for (int ks = 0; ks < kp; ks += 16) {
+              const int t = kSums == 1 ? kT - 1 - i : i;   // (the low terms first: see Split)
               const int pos_k = t * w.row_elems + ks;
               tc_mma(tmem + d * kD + t % kSums * kCols, s_base + (pos_k >> 6) * (kTile * 128) + (pos_k & 63) * 2,
                      at + (ks >> 6) * (kCols * 128) + (ks & 63) * 2, idesc,
-                     t < kT - kSums || ks > 0);
+                     (i > 0 && kSums == 1) || ks > 0);
             }
           sm100::tc_commit(&b_empty[s]);
           sm100::tc_commit(&d_full[d]);
@@ -1260,7 +1261,6 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
   } else {
     const int wm = warp & 3, wn = warp >> 2, g = lane >> 2, c = lane & 3;
     const bool in_place = p.y == p.y_in;
-    bool live = true;
     int nb = 0;
     for_pieces([&](const Piece& q) {
       const int k = q.tile.w, count = q.tile.z;
@@ -1302,7 +1302,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
         float acc[4][4] = {};
         if (k) {
           const int d = nb & 1;
-          live = live && wait_or_flag(&d_full[d], (nb >> 1) & 1, p, &abort_flag);
+          wait_or_flag(&d_full[d], (nb >> 1) & 1, p, &abort_flag);
           ++nb;
           if (some) {
             sm100::tc_fence_after();
