@@ -3,7 +3,7 @@
 #include "rowops.cuh"
 
 namespace wush {
-// Poll limit for bounded mbarrier waits in the GEMM (0 = default); see wush.h.
+// Poll limit for bounded mbarrier waits (0 = default); see wush.h.
 int64_t g_wait_limit_override = 0;
 // ITQ3 mode-1 kernel: 0 tensor cores where the shape allows, 1 CUDA cores; see wush.h.
 int g_itq3_variant = 0;

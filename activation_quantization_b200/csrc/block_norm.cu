@@ -15,11 +15,11 @@
 //    registers (latency counts);
 //  * many rows: persistent CTAs, each with a ring of whole rows in shared memory that
 //    bulk copies fill ahead of it, so that the bytes in flight do not depend on how
-//    many threads wait.  4096 rows x 4096, fp32 y, bf16 stream and h: 28.9 us, 5.81 TB/s;
-//    8192 x 5120 bf16, the norm alone: 30.1 us, 5.57 TB/s; 2048 x 12288 fp32 with layer
-//    norms and a gate per element: 91 us, 4.96 TB/s (its four vectors do not fit beside
+//    many threads wait.  4096 rows x 4096, fp32 y, bf16 stream and h: 29.2 us, 5.75 TB/s;
+//    8192 x 5120 bf16, the norm alone: 30.6 us, 5.48 TB/s; 2048 x 12288 fp32 with layer
+//    norms and a gate per element: 90 us, 5.04 TB/s (its four vectors do not fit beside
 //    the rows and are read from L2 for each row); 1531 x 4097 bf16 with a gate per element, rows
-//    at any element: 23.3 us, 2.70 TB/s (three rows a CTA, about 9000 cycles each).
+//    at any element: 23.9 us, 2.62 TB/s (199 of the 444 CTAs have four rows, the others three).
 #include "rowops.cuh"
 #include "sm100.cuh"
 
@@ -668,9 +668,12 @@ int run(Args& a, bool vec, cudaStream_t st) {
   a.mute = g_wait_limit_override > 0;
   a.polls = a.mute ? g_wait_limit_override : kDefaultPolls;
   a.inv_d = 1.0f / static_cast<float>(a.d);
-  // Few rows, or narrow ones: the ring's set-up would cost more than it hides.  Measured: 7696
-  // rows of 174, 16 bits: 4.9 us and 29 us by the ring; 5536 of 1216, fp32 y, layer norm, gate:
-  // 24.9 and 35.5 us; 4096 of 4096, fp32 y: 38.7 and 29.0 us.
+  // Few rows, or narrow ones: the ring's set-up would cost more than it hides, and a ring CTA's 256
+  // threads have one row of up to 4096 columns at a time, however few it has.  Measured, the ring
+  // second: 7696 rows of 174, 16 bits: 4.9 and 29 us; 5536 of 1216, fp32 y, layer norm, gate:
+  // 24.9 and 35.5; fp32 y, bf16 stream, 4096 rows of 1024: 11.3 and 25.2, of 2048: 20.4 and 26.0;
+  // 16384 rows of 2048: 69.5 and 82.8; 8192 of 2047, 16 bits, gate: 82.9 and 70.0; 4096 of 4096,
+  // fp32 y: 38.7 and 29.0.
   if ((a.rows <= kFewRows && groups <= 1024) || groups <= 256) {
     int threads = round_up(groups, 32);
     if (threads < kMinThreads) threads = threads <= 32 ? 32 : threads <= 64 ? 64 : kMinThreads;

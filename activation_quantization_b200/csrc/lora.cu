@@ -171,10 +171,14 @@ __device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v) {
 // are in flight before any is used.  B and y_in are on their way into L2 while s is computed, a
 // warp asks for several blocks of B (kUnroll) before it multiplies any, and a CTA writes its sums
 // to the others before they meet, so that nobody reads across after it.  1 token, 4096 x 4096,
-// rank 16: 4.4 us, of which about 0.5 go to the adapter's number, 0.5 to the grouping, 0.6 to A,
+// rank 16: 4.5 us, of which about 0.5 go to the adapter's number, 0.5 to the grouping, 0.6 to A,
 // 1.2 to the sums and terms, 0.9 to B and y.  16 tokens, 4096 x 4096, rank 64, one adapter each:
 // 9.3 us, 1.9 TB/s; 200 on 48 adapters of rank 32, 4096 x 12288: 22.0 us, 3.3 TB/s.
-constexpr int few_ctas(int mb) { return mb <= 2 ? 3 : mb <= 8 ? 2 : 1; }   // an SM
+//
+// CTAs an SM.  Three of ranks 17 to 32 have 80 registers a thread and spill some 110 bytes, two of ranks 65
+// to 128 spill 68; with one fewer, which do not spill: 200 tokens on 48 adapters, 4096 x 12288, rank 32,
+// 28.6 us (22.2 so); 32 tokens on 16, 4096 x 4096, rank 32, 7.3 (8.0); 64 on 64, rank 128, 96.9 (44.1).
+constexpr int few_ctas(int mb) { return mb <= 2 ? 3 : mb <= 8 ? 2 : 1; }
 
 template <typename E, int MB>
 __global__ void __launch_bounds__(kFewThreads, few_ctas(MB))
@@ -839,7 +843,7 @@ constexpr int kBk = 128;                                  // columns of d_in a s
 // rounding of the sums (4096 tokens x 12288, rank 128: 5.7e-7 relative to the result; with
 // the second product's low terms last, when both were measured, 1.0e-6, and 2.8e-6 with a chain over a CTA's whole d_in).
 //
-// What bounds it: 4096 tokens x 12288, rank 64, read 113 MB from DRAM and 282 MB from L2 (A
+// What bounds it: 4096 tokens x 12288, rank 64, read 113 MB from DRAM and 277 MB from L2 (A
 // once a tile) in some 31 us, the tensor pipe active for a quarter of it.
 constexpr int kChain = 4;
 
